@@ -49,7 +49,7 @@ typedef struct CUstream_st *cudaStream_t;
 #define ATFLASH_ERR_CUDA (-4)        /* a CUDA runtime/driver call or launch failed */
 #define ATFLASH_ERR_TIMEOUT (-5)     /* a kernel's bounded wait ran out (device status) */
 #define ATFLASH_ERR_ALIGNMENT (-6)   /* a pointer is not 16-byte aligned */
-#define ATFLASH_ERR_BAD_PAGE (-7)    /* a paged decode met a page index past its block-table row or a
+#define ATFLASH_ERR_BAD_PAGE (-7)    /* a paged call met a page index past its block-table row or a
                                         page id outside the pool (device status) */
 
 /* Element types of tensors passed to the GPU calls. */
@@ -342,6 +342,142 @@ int atflash_decode_paged_theta(const void *q, const void *kpages, const void *vp
                                size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Calls around a paged KV cache, for an engine that verifies a tree of drafted
+ * tokens per sequence and step: rotate, append the nodes' keys and values
+ * behind the committed prefix, attend them, keep the accepted ones, copy pages
+ * (no counterpart in the paper; additions of this library).  They share the pool,
+ * block table, seqlens, page_size (a multiple of 64), num_pages and kv_layout
+ * (ATFLASH_KV_NHD or ATFLASH_KV_PACKED) of atflash_decode_paged, bf16, D in
+ * {64, 128}.  Slot s of sequence b is place s % page_size of page
+ * block_table[b*max_pages + s/page_size]; seqlens[b] >= 0 slots hold committed
+ * tokens and node i of a step's tree has slot seqlens[b] + i.
+ *
+ * A slot past the sequence's table row, or a page id outside [0, num_pages), is
+ * found on the device: the call records ATFLASH_ERR_BAD_PAGE in the device
+ * status word, writes nothing to that slot and reads nothing from it.
+ *
+ * Tensors marked "strided" take a HOST array of three element strides {batch,
+ * token, head}, read during the call (dims are contiguous); NULL means contiguous
+ * [B][T][heads][D].  None of these calls allocates or synchronises; all can be
+ * captured into a CUDA graph.
+ */
+
+/*
+ * Rotary positions of queries and keys at given positions.
+ *   q, k        strided [B][T][Hq][D] and [B][T][Hkv][D]; k and k_out may both be
+ *               NULL (Hkv is then ignored).
+ *   q_out, k_out strided, written; may be q and k themselves with the same
+ *               strides (in place), otherwise must not overlap them.
+ *   positions   device int32 [B][T], any values.
+ *   rotary_dim  R, even, 2..D: the first R dims of a head are rotated, the rest
+ *               copied.  Pair r < R/2 is dims (r, r + R/2), or (2r, 2r + 1) when
+ *               interleaved == 1; theta_r = base^(-2r/R).
+ *   scale       multiplies cos and sin (1, or the attention factor of a
+ *               length-extension rule); finite.
+ *   inverse     1: angles negated.  With the same scale this is the gradient of
+ *               the call with inverse == 0.
+ *   dtype       ATFLASH_BF16 or ATFLASH_F32; arithmetic in fp32, angles reduced
+ *               exactly, one rounding at the end.
+ *   D even, 2..256; B*T <= 2^31 - 1; Hq, Hkv <= 32767; tensors 16-byte aligned.
+ * The _theta form takes R/2 frequencies (HOST, as described for the scaled-RoPE
+ * calls above).
+ */
+int atflash_rope_apply(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, void *q_out,
+                       const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides,
+                       const int32_t *positions, int B, int64_t T, int Hq, int Hkv, int D, int rotary_dim,
+                       double rope_base, double scale, int interleaved, int inverse, int dtype, cudaStream_t stream);
+int atflash_rope_apply_theta(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                             void *q_out, const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides,
+                             const int32_t *positions, int B, int64_t T, int Hq, int Hkv, int D, int rotary_dim,
+                             const double *theta, double scale, int interleaved, int inverse, int dtype,
+                             cudaStream_t stream);
+
+/*
+ * New tokens into a paged cache: token i < counts[b] of sequence b goes to slot
+ * seqlens[b] + i, its key rotated by its position and laid out for kv_layout.
+ *   k, v       strided [B][T][Hkv][D] bf16 (un-rotated keys, values), strides
+ *              multiples of 8 elements.
+ *   positions  device int32 [B][T], or NULL: the token's slot.
+ *   counts     device int32 [B] (clamped to 0..T), or NULL: T each.
+ *   kcache_rotated 1, or 0 to store NHD keys un-rotated (as
+ *              atflash_decode_paged's kcache_rotated).
+ * seqlens is not changed.  Slots behind the last token keep their contents.  Two
+ * tokens must not share a slot.
+ */
+int atflash_cache_append(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides, void *kpages,
+                         void *vpages, const int32_t *block_table, const int32_t *seqlens, const int32_t *positions,
+                         const int32_t *counts, int B, int T, int Hkv, int max_pages, int num_pages, int page_size,
+                         int D, double rope_base, int kcache_rotated, int kv_layout, cudaStream_t stream);
+int atflash_cache_append_theta(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                               void *kpages, void *vpages, const int32_t *block_table, const int32_t *seqlens,
+                               const int32_t *positions, const int32_t *counts, int B, int T, int Hkv, int max_pages,
+                               int num_pages, int page_size, int D, const double *theta, int kcache_rotated,
+                               int kv_layout, cudaStream_t stream);
+
+/*
+ * Windowed attention of a tree of drafted tokens over a paged cache whose K is
+ * rotated (as atflash_cache_append writes it).  Node i of sequence b attends the
+ * committed slots m < seqlens[b] (position m) and the nodes j it sees (slot
+ * seqlens[b] + j, position positions[b][j]); pair r of a key enters the score
+ * while positions[b][i] - (the key's position) <= w_r (a negative distance is
+ * kept).  With T = 1 this is atflash_decode_paged for the token in the last slot.
+ *   q          strided [B][T][Hq][D] bf16, un-rotated; rotated here by positions.
+ *   tree_mask  device uint8 [B][T][T], entry (b, i, j) != 0: node i sees node j
+ *              (also its own entry, and entries j > i); NULL: j <= i (a chain).
+ *   positions  device int32 [B][T] >= 0, or NULL: seqlens[b] + i.
+ *   counts     device int32 [B] (clamped to 0..T) nodes of each tree, or NULL: T.
+ *              Rows of q, positions and tree_mask from counts[b] on are not used.
+ *   out        [B][T][Hq][D] (out_dtype); rows i >= counts[b] are left as they
+ *              were.  A node that sees nothing (no committed slot, mask row of
+ *              zeros) gets 0, and -INFINITY as its lse.
+ *   lse        NULL, or [B][Hq][T] fp32: natural log-sum-exp of the scaled scores.
+ *   workspace  device, 16-byte aligned, >= atflash_tree_decode_workspace_bytes();
+ *              calls whose work overlaps on the GPU need one each.
+ * What a key that a node does not see holds (infinities, NaN, stale slots) does
+ * not reach that node.  Pages beyond seqlens[b] + counts[b] are not looked up.
+ * Any Hq / Hkv; B*T*Hq <= 2^31 - 1.
+ */
+size_t atflash_tree_decode_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+int atflash_tree_decode_paged(const void *q, const int64_t *q_strides, const void *kpages, const void *vpages,
+                              const int32_t *block_table, const int32_t *seqlens, const uint8_t *tree_mask,
+                              const int32_t *positions, const int32_t *counts, void *out, float *lse, int B, int T,
+                              int Hq, int Hkv, int max_pages, int num_pages, int page_size, int D, double rope_base,
+                              double k_window, int kv_layout, int out_dtype, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+int atflash_tree_decode_paged_theta(const void *q, const int64_t *q_strides, const void *kpages, const void *vpages,
+                                    const int32_t *block_table, const int32_t *seqlens, const uint8_t *tree_mask,
+                                    const int32_t *positions, const int32_t *counts, void *out, float *lse, int B,
+                                    int T, int Hq, int Hkv, int max_pages, int num_pages, int page_size, int D,
+                                    const double *theta, double k_window, int kv_layout, int out_dtype, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The accepted nodes of each tree moved behind the committed prefix: for
+ * p < accepted[b], slot seqlens[b] + p receives what slot seqlens[b] + path[b][p]
+ * held before the call (every source is read before any slot is written, so
+ * indices may come in any order and more than once).
+ *   path        device int32 [B][M] node indices >= 0, M <= 1024 (otherwise
+ *               ATFLASH_ERR_UNSUPPORTED).  A token whose source does not exist is
+ *               not moved (ATFLASH_ERR_BAD_PAGE in the device status word).
+ *   accepted    device int32 [B], clamped to 0..M.
+ *   new_seqlens NULL, or device int32 [B] written with seqlens[b] + accepted[b];
+ *               must not be seqlens.
+ * The slots moved to must belong to one sequence each.
+ */
+int atflash_cache_compact(void *kpages, void *vpages, const int32_t *block_table, const int32_t *seqlens,
+                          const int32_t *path, const int32_t *accepted, int32_t *new_seqlens, int B, int M, int Hkv,
+                          int max_pages, int num_pages, int page_size, int D, int kv_layout, cudaStream_t stream);
+
+/*
+ * Page dst[e] receives the first tokens[e] tokens (clamped to 0..page_size; NULL:
+ * all) of page src[e], K and V, for e < n (a forked sequence's last page, a pool
+ * being compacted).  src and dst are device int32 [n].  A page must not be the
+ * destination of two copies, nor of one and the source of another.
+ */
+int atflash_cache_copy_pages(void *kpages, void *vpages, const int32_t *src, const int32_t *dst, const int32_t *tokens,
+                             int n, int Hkv, int num_pages, int page_size, int D, int kv_layout, cudaStream_t stream);
+
+/*
  * Decode that allocates nothing (no counterpart in the paper; an addition of
  * this library).  For callers that cannot allocate device memory at the call
  * site, e.g. a serving loop that must never enter the CUDA allocator once it
@@ -371,7 +507,7 @@ int atflash_decode_noalloc(const void *q, const void *kcache, const void *vcache
 /*
  * Device status word of the current device: ATFLASH_OK, ATFLASH_ERR_TIMEOUT
  * when a kernel's bounded wait ran out, or ATFLASH_ERR_BAD_PAGE when a paged
- * decode met a bad page index, since the last clear (the first such event is
+ * call met a bad page index, since the last clear (the first such event is
  * kept).  Synchronises the device.  clear != 0 resets the word.
  */
 int atflash_device_status(int clear);

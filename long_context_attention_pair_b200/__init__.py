@@ -18,7 +18,8 @@ import os
 __all__ = [
     "lib", "prefill", "decode", "pruned_terms", "window_table", "prefill_workspace_bytes",
     "decode_workspace_bytes", "device_status", "AtflashError", "F32", "BF16", "rope_pack", "prefill_packed",
-    "prefill_bf16", "theta_table", "prefill_sparse", "prefill_short_rows",
+    "prefill_bf16", "theta_table", "prefill_sparse", "prefill_short_rows", "rope_apply", "cache_append",
+    "tree_decode_paged", "tree_decode_workspace_bytes", "cache_compact", "cache_copy_pages",
 ]
 
 F32 = 0
@@ -91,6 +92,19 @@ def lib():
         L.atflash_prefill_sparse_theta.argtypes = [vp, vp, vp, vp, vp, i, i, i, i64, i, dp, d, i, vp, vp, sz, vp]
         L.atflash_prefill_short_rows.argtypes = [vp, vp, vp, vp, i, i, i, i64, i, d, d, i, vp, vp]
         L.atflash_prefill_short_rows_theta.argtypes = [vp, vp, vp, vp, i, i, i, i64, i, dp, d, i, vp, vp]
+        rope = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i64, i, i, i, i]
+        L.atflash_rope_apply.argtypes = rope + [d, d, i, i, i, vp]
+        L.atflash_rope_apply_theta.argtypes = rope + [dp, d, i, i, i, vp]
+        append = [vp] * 10 + [i] * 7
+        L.atflash_cache_append.argtypes = append + [d, i, i, vp]
+        L.atflash_cache_append_theta.argtypes = append + [dp, i, i, vp]
+        L.atflash_tree_decode_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.atflash_tree_decode_workspace_bytes.restype = sz
+        tree = [vp] * 11 + [i] * 8
+        L.atflash_tree_decode_paged.argtypes = tree + [d, d, i, i, vp, sz, vp]
+        L.atflash_tree_decode_paged_theta.argtypes = tree + [dp, d, i, i, vp, sz, vp]
+        L.atflash_cache_compact.argtypes = [vp] * 7 + [i] * 8 + [vp]
+        L.atflash_cache_copy_pages.argtypes = [vp] * 5 + [i] * 6 + [vp]
         for f in ("atflash_window_table", "atflash_pruned_terms", "atflash_prefill", "atflash_prefill_ex",
                   "atflash_decode", "atflash_device_status", "atflash_rope_pack", "atflash_prefill_packed",
                   "atflash_prefill_varlen", "atflash_decode_paged", "atflash_theta_table",
@@ -98,7 +112,9 @@ def lib():
                   "atflash_prefill_theta", "atflash_decode_theta", "atflash_prefill_varlen_theta",
                   "atflash_decode_paged_theta", "atflash_prefill_packed_theta", "atflash_prefill_sparse",
                   "atflash_prefill_sparse_theta", "atflash_prefill_short_rows",
-                  "atflash_prefill_short_rows_theta"):
+                  "atflash_prefill_short_rows_theta", "atflash_rope_apply", "atflash_rope_apply_theta",
+                  "atflash_cache_append", "atflash_cache_append_theta", "atflash_tree_decode_paged",
+                  "atflash_tree_decode_paged_theta", "atflash_cache_compact", "atflash_cache_copy_pages"):
             getattr(L, f).restype = i
         _lib = L
     return _lib
@@ -440,9 +456,238 @@ def decode(q, k_cache, v_cache, seqlens, rope_base: float, k_window: float = mat
     return out
 
 
+def _strided(t, name, B, T, heads, D, dtype, written=False):
+    """Pointer and host strides {batch, token, head} of a [B, T, heads, D] tensor whose dims are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (B, T, heads, D):
+        raise ValueError(f"{name} must be [{B}, {T}, {heads}, {D}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    strides = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]  # of a dimension of one, nothing depends on it
+    if strides[3] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if written and any(s == 0 and n > 1 for n, s in zip(t.shape, strides)):
+        raise ValueError(f"{name} is written and must not be an expanded tensor")
+    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*strides[:3])
+
+
+def _ints(t, name, shape):
+    """Pointer of a contiguous int32 CUDA tensor of the given shape, or None."""
+    if t is None:
+        return None
+    if t.dtype != _torch().int32:
+        raise TypeError(f"{name} must be int32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    return _dev(t, name)
+
+
+def _same_device(*tensors):
+    """The one CUDA device of the tensors given, as a context that makes it current."""
+    torch = _torch()
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devs))}")
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    return torch.cuda.device(dev)
+
+
+def _on_stream(stream, *fresh):
+    """Tensors allocated for this call stay reserved until ``stream`` is done with them."""
+    if stream is not None and stream != _torch().cuda.current_stream():
+        for t in fresh:
+            if t is not None:
+                t.record_stream(stream)
+    return _stream_ptr(stream)
+
+
+def _pools(kpages, vpages, page_size, kv_layout, dtype):
+    """(layout code, Hkv, D, num_pages) of a paged cache after checking its shapes."""
+    lay = {"NHD": KV_NHD, "PACKED": KV_PACKED}.get(kv_layout)
+    if lay is None:
+        raise ValueError("kv_layout must be 'NHD' or 'PACKED'")
+    num_pages, P, Hkv, D = vpages.shape
+    if P != page_size:
+        raise ValueError(f"vpages must hold pages of page_size = {page_size} tokens, got {P}")
+    want = (num_pages, P, Hkv, D) if lay == KV_NHD else (num_pages, Hkv, D // 16, P, 16)
+    if tuple(kpages.shape) != want:
+        raise ValueError(f"kpages must be {list(want)} for kv_layout {kv_layout!r}, got {tuple(kpages.shape)}")
+    if kpages.dtype != dtype or vpages.dtype != dtype:
+        raise TypeError("kpages and vpages must be bfloat16")
+    return lay, Hkv, D, num_pages
+
+
+def _rope_arg(name, rope_base, theta, dims):
+    """The C call (base or frequency table) and its frequency argument."""
+    if theta is None:
+        return getattr(lib(), name), name, float(rope_base)
+    return getattr(lib(), name + "_theta"), name + "_theta", _theta_arg(theta, dims)
+
+
+def rope_apply(q, k, positions, rope_base: float, *, rotary_dim=None, interleaved: bool = False, scale: float = 1.0,
+               inverse: bool = False, out_q=None, out_k=None, stream=None, theta=None):
+    """Rotary positions of queries and keys at given positions.
+
+    q [B, T, Hq, D] and k [B, T, Hkv, D] (or None) bf16 or fp32, any strides with
+    contiguous dims; positions int32 [B, T].  The first ``rotary_dim`` dims (all by
+    default) are rotated as pairs (r, r + R/2), or (2r, 2r + 1) when ``interleaved``,
+    cos and sin multiplied by ``scale``; the rest is copied.  ``inverse`` negates the
+    angles: the gradient of the same call without it.  ``out_q=q, out_k=k`` works in
+    place.  ``theta`` (R/2 frequencies) replaces base^(-2r/R).  Returns (q, k) rotated,
+    or the rotated q alone when k is None.
+    """
+    torch = _torch()
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2] if k is not None else 0
+    R = D if rotary_dim is None else int(rotary_dim)
+    dt = _dtype_code(q)
+    new_q, new_k = out_q is None, out_k is None and k is not None
+    with _same_device(q, k, positions, out_q, out_k):
+        pos = _ints(positions, "positions", (B, T))
+        qp, qs = _strided(q, "q", B, T, Hq, D, q.dtype)
+        if new_q:
+            out_q = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+        oqp, oqs = _strided(out_q, "out_q", B, T, Hq, D, q.dtype, True)
+        kp = ks = okp = oks = None
+        if k is not None:
+            kp, ks = _strided(k, "k", B, T, Hkv, D, q.dtype)
+            if new_k:
+                out_k = torch.empty((B, T, Hkv, D), dtype=q.dtype, device=q.device)
+            okp, oks = _strided(out_k, "out_k", B, T, Hkv, D, q.dtype, True)
+        fn, name, rope = _rope_arg("atflash_rope_apply", rope_base, theta, R)
+        sp = _on_stream(stream, out_q if new_q else None, out_k if new_k else None)
+        _check(fn(qp, qs, kp, ks, oqp, oqs, okp, oks, pos, B, T, Hq, Hkv, D, R, rope, float(scale), int(bool(interleaved)),
+                  int(bool(inverse)), dt, sp), name)
+    return out_q if k is None else (out_q, out_k)
+
+
+def cache_append(k, v, kpages, vpages, block_table, seqlens, page_size: int, rope_base: float, *, positions=None,
+                 counts=None, kcache_rotated: bool = True, kv_layout: str = "NHD", stream=None, theta=None):
+    """New tokens into a paged cache, in place.
+
+    k, v [B, T, Hkv, D] bf16 (un-rotated keys; strides multiples of 8); token i <
+    counts[b] (all T by default) of sequence b goes to slot seqlens[b] + i, its key
+    rotated by positions[b, i] (its slot by default).  Pools, block_table and
+    kv_layout as for ``decode_paged``.  ``kcache_rotated=False`` stores NHD keys
+    un-rotated.  ``seqlens`` is not changed.
+    """
+    torch = _torch()
+    B, T, Hkv, D = k.shape
+    with _same_device(k, v, kpages, vpages, block_table, seqlens, positions, counts):
+        lay, Hp, Dp, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+        if (Hp, Dp) != (Hkv, D):
+            raise ValueError(f"the pools hold [{Hp}, {Dp}] a token, k [{Hkv}, {D}]")
+        kp, ks = _strided(k, "k", B, T, Hkv, D, torch.bfloat16)
+        vp, vs = _strided(v, "v", B, T, Hkv, D, torch.bfloat16)
+        fn, name, rope = _rope_arg("atflash_cache_append", rope_base, theta, D)
+        _check(fn(kp, ks, vp, vs, _dev(kpages, "kpages"), _dev(vpages, "vpages"),
+                  _ints(block_table, "block_table", (B, block_table.shape[-1])), _ints(seqlens, "seqlens", (B,)),
+                  _ints(positions, "positions", (B, T)), _ints(counts, "counts", (B,)), B, T, Hkv, block_table.shape[-1],
+                  num_pages, int(page_size), D, rope, int(bool(kcache_rotated)), lay, _stream_ptr(stream)), name)
+
+
+def tree_decode_workspace_bytes(B, T, Hq, Hkv, D) -> int:
+    return int(lib().atflash_tree_decode_workspace_bytes(B, T, Hq, Hkv, D))
+
+
+def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, rope_base: float,
+                      k_window: float = math.inf, *, tree_mask=None, positions=None, counts=None,
+                      kv_layout: str = "NHD", out=None, out_dtype=None, lse=None, return_lse: bool = False,
+                      workspace=None, stream=None, theta=None):
+    """Windowed attention of a tree of drafted tokens over a paged cache with rotated keys.
+
+    q [B, T, Hq, D] bf16 (un-rotated; any strides with contiguous dims): node i of
+    sequence b sits at positions[b, i] (seqlens[b] + i by default), attends the
+    seqlens[b] committed slots and the nodes j with tree_mask[b, i, j] ([B, T, T]
+    uint8 or bool; j <= i by default), whose keys and values ``cache_append`` put in
+    slots seqlens[b] + j.  Only the first counts[b] nodes (all T by default) take part;
+    other rows of ``out`` are left as they were (zeros when allocated here).  Returns
+    out [B, T, Hq, D]; with ``return_lse`` or an ``lse`` buffer, (out, lse [B, Hq, T]
+    fp32).  A node that sees nothing gets 0 and -inf.  ``workspace``:
+    ``tree_decode_workspace_bytes`` bytes, not shared by calls that overlap.
+    """
+    torch = _torch()
+    B, T, Hq, D = q.shape
+    with _same_device(q, kpages, vpages, block_table, seqlens, tree_mask, positions, counts, out, lse, workspace):
+        lay, Hkv, Dp, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+        if Dp != D:
+            raise ValueError(f"the pools hold heads of {Dp} dims, q of {D}")
+        qp, qs = _strided(q, "q", B, T, Hq, D, torch.bfloat16)
+        mask = None
+        if tree_mask is not None:
+            if tree_mask.dtype not in (torch.bool, torch.uint8):
+                raise TypeError("tree_mask must be uint8 or bool")
+            if tuple(tree_mask.shape) != (B, T, T):
+                raise ValueError(f"tree_mask must be [{B}, {T}, {T}], got {tuple(tree_mask.shape)}")
+            mask = _dev(tree_mask, "tree_mask")
+        make = torch.empty if counts is None else torch.zeros
+        fresh = [None, None, None]
+        if out is None:
+            out = fresh[0] = make((B, T, Hq, D), dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+        elif tuple(out.shape) != (B, T, Hq, D):
+            raise ValueError(f"out must be [{B}, {T}, {Hq}, {D}], got {tuple(out.shape)}")
+        if lse is None and return_lse:
+            lse = fresh[1] = make((B, Hq, T), dtype=torch.float32, device=q.device)
+        elif lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T)):
+            raise ValueError(f"lse must be float32 [{B}, {Hq}, {T}]")
+        need = tree_decode_workspace_bytes(B, T, Hq, Hkv, D)
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = fresh[2] = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        fn, name, rope = _rope_arg("atflash_tree_decode_paged", rope_base, theta, D)
+        sp = _on_stream(stream, *fresh)
+        _check(fn(qp, qs, _dev(kpages, "kpages"), _dev(vpages, "vpages"),
+                  _ints(block_table, "block_table", (B, block_table.shape[-1])), _ints(seqlens, "seqlens", (B,)), mask,
+                  _ints(positions, "positions", (B, T)), _ints(counts, "counts", (B,)), _dev(out, "out"),
+                  _dev(lse, "lse") if lse is not None else None, B, T, Hq, Hkv, block_table.shape[-1], num_pages,
+                  int(page_size), D, rope, float(k_window), lay, _dtype_code(out), _dev(workspace, "workspace"), need,
+                  sp), name)
+    return (out, lse) if lse is not None else out
+
+
+def cache_compact(kpages, vpages, block_table, seqlens, path, accepted, page_size: int, *, new_seqlens=None,
+                  kv_layout: str = "NHD", stream=None):
+    """The accepted nodes of each tree moved behind the committed prefix, in place.
+
+    For p < accepted[b] (int32 [B]) slot seqlens[b] + p receives what slot seqlens[b] +
+    path[b, p] (int32 [B, M], M <= 1024) held before the call.  Returns new_seqlens =
+    seqlens + accepted (int32 [B], a new tensor unless given; not ``seqlens`` itself).
+    """
+    torch = _torch()
+    B, M = path.shape
+    with _same_device(kpages, vpages, block_table, seqlens, path, accepted, new_seqlens):
+        lay, Hkv, D, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+        fresh = None
+        if new_seqlens is None:
+            new_seqlens = fresh = torch.empty((B,), dtype=torch.int32, device=seqlens.device)
+        sp = _on_stream(stream, fresh)
+        _check(lib().atflash_cache_compact(
+            _dev(kpages, "kpages"), _dev(vpages, "vpages"), _ints(block_table, "block_table", (B, block_table.shape[-1])),
+            _ints(seqlens, "seqlens", (B,)), _ints(path, "path", (B, M)), _ints(accepted, "accepted", (B,)),
+            _ints(new_seqlens, "new_seqlens", (B,)), B, M, Hkv, block_table.shape[-1], num_pages, int(page_size), D, lay,
+            sp), "atflash_cache_compact")
+    return new_seqlens
+
+
+def cache_copy_pages(kpages, vpages, src, dst, page_size: int, *, tokens=None, kv_layout: str = "NHD", stream=None):
+    """Page dst[e] receives the first tokens[e] tokens (all by default) of page src[e], K and
+    V, in place (int32 [n] each).  A page must not be the destination of two copies, nor
+    of one and the source of another."""
+    torch = _torch()
+    n = src.numel()
+    with _same_device(kpages, vpages, src, dst, tokens):
+        lay, Hkv, D, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+        _check(lib().atflash_cache_copy_pages(
+            _dev(kpages, "kpages"), _dev(vpages, "vpages"), _ints(src, "src", (n,)), _ints(dst, "dst", (n,)),
+            _ints(tokens, "tokens", (n,)), n, Hkv, num_pages, int(page_size), D, lay, _stream_ptr(stream)),
+            "atflash_cache_copy_pages")
+
+
 def device_status(clear: bool = True) -> int:
     """ATFlash device status word: 0, -5 after a kernel's bounded wait ran out, or
-    -7 after a paged decode met a bad page index (the first event is kept)."""
+    -7 after a paged call met a bad page index (the first event is kept)."""
     return int(lib().atflash_device_status(1 if clear else 0))
 
 

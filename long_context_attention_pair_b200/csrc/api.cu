@@ -199,7 +199,7 @@ const char *atflash_status_string(int status) {
         case ATFLASH_ERR_CUDA: return "CUDA runtime or launch error";
         case ATFLASH_ERR_TIMEOUT: return "a kernel's bounded wait ran out";
         case ATFLASH_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
-        case ATFLASH_ERR_BAD_PAGE: return "a paged decode met a page index outside its block table or pool";
+        case ATFLASH_ERR_BAD_PAGE: return "a paged call met a page index outside its block table or pool";
         default: return "unknown status";
     }
 }

@@ -6,7 +6,7 @@
 // into the device status word (first writer wins); the host maps any value at
 // or above the base to ATFLASH_ERR_TIMEOUT.
 #define ATFLASH_DEVICE_TIMEOUT_BASE 1000
-// A paged decode that met a page index past its block-table row, or a page id
+// A paged call that met a page index past its block-table row, or a page id
 // outside the pool, writes this value (first writer wins); the host maps it to
 // ATFLASH_ERR_BAD_PAGE.
 #define ATFLASH_DEVICE_BAD_PAGE 2000
