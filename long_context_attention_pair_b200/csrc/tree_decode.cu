@@ -20,6 +20,14 @@
 // otherwise it leaves (max, sum, unscaled output) in the workspace, at most twice
 // per CTA (its first and its last item), and tree_merge_kernel joins them.
 //
+// Softmax.  Two sets of four warps take alternate key tiles, each with a running
+// max, sum and O accumulator of its own (joined at the end of a run of tiles), so
+// a set has two tile times for the chain S -> P -> PV and no row is shared between
+// warps.  NC is the number of a tile's columns that one warp takes: with at most 32
+// (64) rows the queries are repeated in all four (both halves) of the MMA's 128
+// rows and each copy takes a quarter (half) of the columns, P being zero in the
+// others, which shortens the chain where few rows leave the lanes empty.
+//
 // Windows.  Inside one tile the distances span [d_min, d_max]: pairs r < r_lo are
 // pruned for every cell and their packed chunks not loaded, pairs r >= r_full are
 // kept for every cell and go through the MMA, and the boundary pairs between are
@@ -31,12 +39,12 @@
 // V's own), which moves an output by at most 2^-8 of sum p |v|; sums, maxima and
 // O are fp32.
 //
-// 12 warps: 0-7 softmax (warp 4 hc + q4: TMEM lane quarter q4, columns 64 hc..;
-// the two warps of a row exchange maxima per tile), 8 TMA producer, 9 QK issuer,
-// 10 fix-up (zeroes boundary pairs in K, stages them, clears V behind the last
-// node), 11 PV issuer.  S and P are double-buffered in TMEM, so the next tile's QK
-// runs under this tile's softmax.  Every mbarrier wait is bounded; on expiry the
-// CTA records ATFLASH_ERR_TIMEOUT, lets its copies and MMAs finish and exits.
+// 16 warps: 0-7 softmax (set = warp / 4, TMEM lane quarter warp % 4), 8 K producer,
+// 9 QK issuer, 10 fix-up (stages boundary pairs, zeroes them in K), 11 PV issuer,
+// 12 V producer, 13 scheduler (publishes the runs of tiles through a ring), 14-15
+// tails (mask bits of tiles with nodes, V behind the last node cleared).  Every
+// mbarrier wait is bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its
+// copies and MMAs finish and exits.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -48,55 +56,69 @@ namespace tree {
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kSoft = 8;
-constexpr int kProducer = 8, kQk = 9, kFix = 10, kPv = 11;
-constexpr int kThreads = 32 * 12;
-// Registers: 168 per thread at launch; the last warpgroup drops to 96 and the two
-// softmax warpgroups rise to 200, within the launch's total (checked here and,
+constexpr int kProducer = 8, kQk = 9, kFix = 10, kPv = 11, kVProducer = 12, kSched = 13, kTail = 14;
+constexpr int kThreads = 32 * 16;
+// Registers: 128 per thread at launch; the last two warpgroups drop to 80 and the
+// two softmax warpgroups rise to 176, within the launch's total (checked here and,
 // against the compiled kernel, at launch).
-constexpr int kLaunchRegs = 168, kSoftRegs = 200, kOtherRegs = 96;
-static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
+constexpr int kLaunchRegs = 128, kSoftRegs = 176, kOtherRegs = 80;
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
 constexpr int kStaged = 16;      // boundary pairs staged per tile (at least one natural K-step)
+constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 template <int D>
 struct Cfg {
     static constexpr int H = D / 2;
     static constexpr int C = D / 16;                 // K-steps
-    static constexpr int ST = D == 128 ? 2 : 4;      // K and V stages: 128 KB in flight or in use
+    static constexpr int ST = D == 128 ? 2 : 4;      // K and V stages: 128 KB in flight or in use (even: a stage serves one set)
     static constexpr int TileBytes = kBM * D * 2;    // Q hi, Q lo, a K stage, a V stage
-    static constexpr int OffQ = 0;
+    static constexpr int OffQ = 0;                   // also the fp32 exchange of repeated rows: 128 x D x 4
     static constexpr int OffK = OffQ + 2 * TileBytes;
     static constexpr int OffV = OffK + ST * TileBytes;
     static constexpr int OffStage = OffV + ST * TileBytes;       // [ST][kStaged][128] words (k_r, k_{r+H})
     static constexpr int StageBytes = kStaged * kBN * 4;
     static constexpr int OffKpos = OffStage + ST * StageBytes;   // [ST][128] key positions
-    static constexpr int OffCtl = OffKpos + ST * kBN * 4;
-    static constexpr int CtlBytes = 5120;
+    static constexpr int OffMask = OffKpos + ST * kBN * 4;       // [2][128] rows of 128 mask bits, one per node
+    static constexpr int OffCtl = OffMask + 2 * kBM * 16;
+    static constexpr int CtlBytes = 4096;
     static constexpr int Request = OffCtl + CtlBytes + 1024;
     static_assert(Request <= 232448, "shared memory of one CTA");
-    static constexpr uint32_t TmemS = 0, TmemO = 256, TmemP = 384, TmemCols = 512;
+    // TMEM: S of set t at 128 t, O at 256 + D t.  P (64 columns of bf16 pairs): beside them for
+    // D = 64; for D = 128 over S, which its warps have read by then.
+    static constexpr bool PoverS = D == 128;
+    static constexpr uint32_t TmemO = 256, TmemCols = 512;
+    static constexpr uint32_t TmemP = PoverS ? 0 : 384, TmemPStep = PoverS ? 128 : 64;
+};
+
+// One run of key tiles of one item.
+struct Segment {
+    int b, h;         // sequence, KV head
+    int L, nodes;
+    int row0, rows;   // this CTA's rows of the problem; rows == 0: no more runs
+    int tile0, ntile, tiles;
+    int pmin, pmax;   // positions of the row tile's nodes
+    int kmin;         // smallest position of a node (as a key)
 };
 
 struct Ctl {
+    uint64_t seg_full[kRing], seg_empty[kRing];
     uint64_t q_ready;
     uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
     uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
-    uint64_t drain;
-    uint64_t xbar[4], lbar[4];       // per lane quarter: both column halves have posted
+    uint64_t m_full[2], m_empty[2];
+    uint64_t drain, soft_bar;
     uint32_t tmem_base;
     int abort_flag;
-    int first_b;
-    int64_t first_off, run;          // this group's first unit inside sequence first_b, and its number of units
-    int64_t total;
+    Segment seg[kRing];
     int band[4][2];                  // (r_lo, r_full) of the tile in each stage
-    int nf_seg[8];                   // segment (mod 8) whose tree holds a non-finite value
+    int nf_seg[8];                   // run (mod 8) whose tree holds a non-finite value
     int w[64];
-    float xval[4][2][2][32];         // (quarter, tile parity, column half, lane)
-    float lval[4][2][32];
+    float2 stat[2][kBM];             // (max, sum) of each set and MMA row
 };
-static_assert(sizeof(Ctl) <= 5120, "control block outgrew its space");
+static_assert(sizeof(Ctl) <= 4096, "control block outgrew its space");
 
 // What the scheduler needs to know of a sequence.
 struct Seq {
@@ -135,49 +157,6 @@ __device__ __forceinline__ int64_t units_before(const TreeArgs &a, const Shape &
 __device__ __forceinline__ int active_groups(int64_t total, int groups) { return total < groups ? (int)total : groups; }
 __device__ __forceinline__ int64_t first_unit(int64_t total, int active, int g) { return (int64_t)g * total / active; }
 
-// One run of key tiles of one item, as every warp of a CTA walks them.
-struct Segment {
-    int b, h;         // sequence, KV head
-    int64_t L;
-    int nodes;
-    int row0, rows;   // this CTA's rows of the problem (rows <= 0: none)
-    int tile0, ntile, tiles;
-};
-struct Walk {
-    int b;
-    int64_t off, left;
-    Seq s;
-    __device__ __forceinline__ void init(const TreeArgs &a, const Shape &sh, const Ctl *ctl) {
-        b = ctl->first_b;
-        off = ctl->first_off;
-        left = ctl->run;
-        if (left > 0) s = seq_of(a, sh, b);
-    }
-    __device__ __forceinline__ bool next(const TreeArgs &a, const Shape &sh, int member, Segment &g) {
-        while (left > 0) {
-            if (off >= units_of(s, sh.Hkv)) {
-                off = 0;
-                s = seq_of(a, sh, ++b);
-                continue;
-            }
-            const int item = (int)(off / s.tiles);
-            g.b = b;
-            g.h = item / s.groups;
-            g.L = s.L;
-            g.nodes = s.nodes;
-            g.row0 = (item % s.groups * sh.R + member) * kBM;
-            g.rows = min(kBM, s.nodes * sh.G - g.row0);
-            g.tiles = s.tiles;
-            g.tile0 = (int)(off - (int64_t)item * s.tiles);
-            g.ntile = (int)min((int64_t)(s.tiles - g.tile0), left);
-            off += g.ntile;
-            left -= g.ntile;
-            if (g.rows > 0) return true;
-        }
-        return false;
-    }
-};
-
 // Offset of 32-bit word `word` of row `row` in a K-step of 128 rows x 32 bytes
 // (SWIZZLE_32B), and of element d in 128-byte rows of 64 dims (SWIZZLE_128B, one
 // 16 KB block per 64 dims).
@@ -207,6 +186,15 @@ __device__ __forceinline__ void store_pair(uint8_t *tile, int row, int r, uint32
         *reinterpret_cast<uint16_t *>(tile + sw128_off(row, r + D / 2)) = (uint16_t)(x >> 16);
     }
 }
+// Pairs of one MMA K-step (packed) or of a K-step and its partner (natural).
+template <bool kPacked>
+constexpr int kPairsPerStep = kPacked ? 8 : 16;
+// Whether the fix-up warp touches a tile: boundary pairs to stage, or pairs that
+// its first K-step must not see.
+template <bool kPacked>
+__device__ __forceinline__ bool needs_fix(int r_lo, int r_full) {
+    return r_lo < r_full || r_full % kPairsPerStep<kPacked> != 0;
+}
 
 __device__ __forceinline__ int first_kept(const int *w, int H, int64_t d) {
     int lo = 0, hi = H;
@@ -217,6 +205,16 @@ __device__ __forceinline__ int first_kept(const int *w, int H, int64_t d) {
     return lo;
 }
 
+// Bounded wait of a whole warp.  The first, suspended attempt covers every wait of
+// a healthy pipeline without reading the (slow) global timer.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WaitCtl &wc, uint32_t site) {
+    bool ok = mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 20000u);
+    if (!ok) {
+        wc.site = site;
+        ok = mbar_wait(bar, parity, wc);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity))
@@ -224,96 +222,116 @@ __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint6
     return true;
 }
 
-// Position of node i.
-__device__ __forceinline__ int64_t node_pos(const TreeArgs &a, const Segment &g, int i) {
-    return a.positions ? (int64_t)a.positions[(size_t)g.b * a.T + i] : g.L + i;
+// The runs of tiles, in order, as every warp but the scheduler sees them.
+struct Runs {
+    Ctl *ctl;
+    int n = 0;  // runs taken
+    __device__ __forceinline__ explicit Runs(Ctl *c) : ctl(c) {}
+    __device__ __forceinline__ const Segment &now() const { return ctl->seg[(n - 1) % kRing]; }
+    __device__ __forceinline__ bool next(WaitCtl &wc, bool &ok) {
+        ok = wait(&ctl->seg_full[n % kRing], (n / kRing) & 1, wc, 59);
+        if (!ok) return false;
+        ++n;
+        return now().rows > 0;
+    }
+    __device__ __forceinline__ void done(int lane) {  // every lane has read what it needs of the run
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->seg_empty[(n - 1) % kRing]);
+    }
+};
+
+__device__ __forceinline__ int node_pos(const TreeArgs &a, int b, int L, int i) {
+    return a.positions ? a.positions[(size_t)b * a.T + i] : L + i;
 }
-// Whether node i sees node j (both below g.nodes).
-__device__ __forceinline__ bool node_sees(const TreeArgs &a, const Segment &g, int i, int j) {
-    return a.mask ? a.mask[((size_t)g.b * a.T + i) * a.T + j] != 0 : j <= i;
+// Whether node i sees node j (both below the sequence's count).
+__device__ __forceinline__ bool node_sees(const TreeArgs &a, int b, int i, int j) {
+    return a.mask ? a.mask[((size_t)b * a.T + i) * a.T + j] != 0 : j <= i;
 }
 
-template <int D, bool kPacked>
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Non-finite values of the nodes that row `tok` sees among the slots of tiles
+// [tile0, tile0 + ntile), added to its output dims d0 .. d0 + N - 1 (the fix-up of the
+// values that the tail warps took out of the MMA's operand).
+template <int N>
+__device__ __noinline__ void add_nonfinite(const TreeArgs &a, const Segment &g, int D, int tok, int d0, float *o) {
+    const int64_t end = (int64_t)g.L + g.nodes;
+    const int64_t lo = max((int64_t)g.L, (int64_t)g.tile0 * kBN), hi = min(end, (int64_t)(g.tile0 + g.ntile) * kBN);
+    for (int64_t slot = lo; slot < hi; ++slot) {
+        if (!node_sees(a, g.b, tok, (int)(slot - g.L))) continue;
+        const int page = page_of(a.pk, g.b, slot, a.status);
+        if (page < 0) continue;
+        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.vpages) +
+                                 (((size_t)page * a.pk.page_size + slot % a.pk.page_size) * a.Hkv + g.h) * D + d0;
+        for (int i = 0; i < N; ++i) {
+            const float x = __bfloat162float(v[i]);
+            if (!isfinite(x)) o[i] += x;
+        }
+    }
+}
+
+template <int D, bool kPacked, int NC>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ TreeArgs a, const __grid_constant__ Shape sh,
                        const __grid_constant__ WindowParams wp, const __grid_constant__ RopeTurns rt, int box_keys) {
     using F = Cfg<D>;
     constexpr int H = F::H, C = F::C, ST = F::ST;
+    constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
+    constexpr int CW = NC < 64 ? NC : 64;               // columns in registers at a time
+    constexpr int kPer = kPairsPerStep<kPacked>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + F::OffQ, *sK = smem + F::OffK, *sV = smem + F::OffV;
     uint32_t *sStage = reinterpret_cast<uint32_t *>(smem + F::OffStage);
     int *sKpos = reinterpret_cast<int *>(smem + F::OffKpos);
+    uint4 *sMask = reinterpret_cast<uint4 *>(smem + F::OffMask);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + F::OffCtl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int member = blockIdx.x % sh.R, group = blockIdx.x / sh.R;
 
     if (warp == kQk) {
         tmem_alloc(&ctl->tmem_base, F::TmemCols);
         tmem_relinquish();
     } else if (warp == kPv) {
         if (lane == 0) {
+            for (int s = 0; s < kRing; ++s) {
+                mbar_init(&ctl->seg_full[s], 1);
+                mbar_init(&ctl->seg_empty[s], kThreads / 32 - 1);
+            }
             mbar_init(&ctl->q_ready, kSoft);
             for (int s = 0; s < ST; ++s) {
                 mbar_init(&ctl->k_full[s], 1);
                 mbar_init(&ctl->k_ready[s], 1);
-                mbar_init(&ctl->k_empty[s], 1 + kSoft);
+                mbar_init(&ctl->k_empty[s], 1 + 4);
                 mbar_init(&ctl->v_full[s], 1);
-                mbar_init(&ctl->v_ready[s], 1);
+                mbar_init(&ctl->v_ready[s], 2);
                 mbar_init(&ctl->v_empty[s], 1);
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&ctl->s_full[s], 1);
-                mbar_init(&ctl->s_read[s], kSoft);
-                mbar_init(&ctl->p_full[s], kSoft);
+                mbar_init(&ctl->s_read[s], 4);
+                mbar_init(&ctl->p_full[s], 4);
                 mbar_init(&ctl->o_done[s], 1);
+                mbar_init(&ctl->m_full[s], 2);
+                mbar_init(&ctl->m_empty[s], 4);
             }
             mbar_init(&ctl->drain, 2);
-            for (int q = 0; q < 4; ++q) {
-                mbar_init(&ctl->xbar[q], 2);
-                mbar_init(&ctl->lbar[q], 2);
-            }
+            mbar_init(&ctl->soft_bar, kSoft);
             ctl->abort_flag = 0;
             for (int s = 0; s < 8; ++s) ctl->nf_seg[s] = -1;
             fence_mbar_init();
         }
     } else if (warp == kProducer) {
-        // This group's run of units: the total, then the sequence that holds the first.
-        const int64_t total = units_before(a, sh, sh.B);
-        const int active = active_groups(total, sh.groups);
-        const int64_t u0 = group < active ? first_unit(total, active, group) : 0;
-        const int64_t u1 = group < active ? first_unit(total, active, group + 1) : 0;
-        int64_t base = 0;
-        int found = 0;
-        int64_t off = 0;
-        for (int b0 = 0; b0 < sh.B && u1 > u0; b0 += 32) {
-            const int b = b0 + lane;
-            const int64_t n = b < sh.B ? units_of(seq_of(a, sh, b), sh.Hkv) : 0;
-            int64_t incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const bool here = u0 >= base + incl - n && u0 < base + incl;
-            const uint32_t m = __ballot_sync(0xffffffffu, here);
-            if (m) {
-                const int src = __ffs(m) - 1;
-                found = b0 + src;
-                off = u0 - __shfl_sync(0xffffffffu, base + incl - n, src);
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) {
-            ctl->first_b = found;
-            ctl->first_off = off;
-            ctl->run = u1 - u0;
-            ctl->total = total;
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
-        }
+        if (lane == 0) prefetch_tmap(&tm_k);
+    } else if (warp == kVProducer) {
+        if (lane == 0) prefetch_tmap(&tm_v);
     } else if (warp == kFix) {
         for (int r = lane; r < H; r += 32) ctl->w[r] = wp.w[r];
     }
@@ -324,122 +342,167 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl->tmem_base;
     const int *w = ctl->w;
     WaitCtl wc{&ctl->abort_flag, a.status, a.limit_ns, 40};
-    Walk walk;
-    walk.init(a, sh, ctl);
-    Segment g;
-    int it = 0, seg = 0;  // tiles and segments this CTA has walked
+    Runs runs(ctl);
+    int it = 0;  // tiles this CTA has walked
     bool ok = true;
 
     if (warp >= kSoft) setmaxnreg_dec<kOtherRegs>();
-    if (warp == kProducer) {
-        // ------------------------------------------------------------ producer
-        int last[ST];
+    if (warp == kSched) {
+        // ------------------------------------------------------------ scheduler
+        // This group's run of units: the total, then the sequence that holds the first.
+        const int member = blockIdx.x % sh.R, group = blockIdx.x / sh.R;
+        const int64_t total = units_before(a, sh, sh.B);
+        const int active = active_groups(total, sh.groups);
+        const int64_t u0 = group < active ? first_unit(total, active, group) : 0;
+        int64_t left = (group < active ? first_unit(total, active, group + 1) : 0) - u0, off = 0, base = 0;
+        int b = 0;
+        for (int b0 = 0; b0 < sh.B && left > 0; b0 += 32) {
+            const int64_t n = b0 + lane < sh.B ? units_of(seq_of(a, sh, b0 + lane), sh.Hkv) : 0;
+            int64_t incl = n;
 #pragma unroll
-        for (int s = 0; s < ST; ++s) last[s] = -1;
-        int lastv = -1;
-        for (; ok && walk.next(a, sh, member, g); ++seg) {
-            // Positions of this row tile's nodes, and the nearest position of any node as a key.
-            const int i0 = g.row0 / sh.G, i1 = (g.row0 + g.rows - 1) / sh.G;
-            int64_t pmin, pmax, kmin;
-            if (a.positions) {
-                int lo = INT32_MAX, hi = INT32_MIN, kl = INT32_MAX;
-                for (int i = lane; i < g.nodes; i += 32) {
-                    const int p = a.positions[(size_t)g.b * a.T + i];
-                    kl = min(kl, p);
-                    if (i >= i0 && i <= i1) lo = min(lo, p), hi = max(hi, p);
-                }
-                pmin = __reduce_min_sync(0xffffffffu, lo);
-                pmax = __reduce_max_sync(0xffffffffu, hi);
-                kmin = __reduce_min_sync(0xffffffffu, kl);
-            } else {
-                pmin = g.L + i0, pmax = g.L + i1, kmin = g.L;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
             }
-            const int64_t end = g.L + g.nodes;
+            const uint32_t m = __ballot_sync(0xffffffffu, u0 >= base + incl - n && u0 < base + incl);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                b = b0 + src;
+                off = u0 - __shfl_sync(0xffffffffu, base + incl - n, src);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        Seq s{};
+        if (left > 0) s = seq_of(a, sh, b);
+        for (int n = 0; ok; ++n) {
+            Segment g{};
+            while (left > 0) {
+                if (off >= units_of(s, sh.Hkv)) {
+                    off = 0;
+                    s = seq_of(a, sh, ++b);
+                    continue;
+                }
+                const int item = (int)(off / s.tiles);
+                g.b = b;
+                g.h = item / s.groups;
+                g.L = (int)s.L;
+                g.nodes = s.nodes;
+                g.row0 = (item % s.groups * sh.R + member) * kBM;
+                g.rows = min(kBM, s.nodes * sh.G - g.row0);
+                g.tiles = s.tiles;
+                g.tile0 = (int)(off - (int64_t)item * s.tiles);
+                g.ntile = (int)min((int64_t)(s.tiles - g.tile0), left);
+                off += g.ntile;
+                left -= g.ntile;
+                if (g.rows > 0) break;
+                g.rows = 0;  // this CTA's row tile does not exist in this item
+            }
+            if (g.rows > 0) {
+                const int i0 = g.row0 / sh.G, i1 = (g.row0 + g.rows - 1) / sh.G;
+                if (a.positions) {
+                    int lo = INT32_MAX, hi = INT32_MIN, kl = INT32_MAX;
+                    for (int i = lane; i < g.nodes; i += 32) {
+                        const int p = a.positions[(size_t)b * a.T + i];
+                        kl = min(kl, p);
+                        if (i >= i0 && i <= i1) lo = min(lo, p), hi = max(hi, p);
+                    }
+                    g.pmin = __reduce_min_sync(0xffffffffu, lo);
+                    g.pmax = __reduce_max_sync(0xffffffffu, hi);
+                    g.kmin = __reduce_min_sync(0xffffffffu, kl);
+                } else {
+                    g.pmin = g.L + i0, g.pmax = g.L + i1, g.kmin = g.L;
+                }
+            }
+            if (!(ok = wait(&ctl->seg_empty[n % kRing], ((n / kRing) & 1) ^ 1, wc, 60))) break;
+            if (lane == 0) {
+                ctl->seg[n % kRing] = g;
+                mbar_arrive(&ctl->seg_full[n % kRing]);
+            }
+            __syncwarp();
+            if (g.rows == 0) break;
+        }
+    } else if (warp == kProducer || warp == kVProducer) {
+        // ------------------------------------------- producers of K and of V
+        const bool v = warp == kVProducer;
+        uint64_t *full = v ? ctl->v_full : ctl->k_full, *empty = v ? ctl->v_empty : ctl->k_empty;
+        const int u = lane >> 1, hf = lane & 1;  // lane = (K-step or dim group, half of the tile)
+        const uint32_t P = (uint32_t)a.pk.page_size;
+        while (ok && runs.next(wc, ok)) {
+            const Segment g = runs.now();
+            runs.done(lane);
+            const int64_t end = (int64_t)g.L + g.nodes;
             int r_lo = H, r_full = H;
-            int page = -1;  // page of half-tile (tile0 & ~15) * 2 + lane
+            int page = -1;  // page of half-tile 2 * (j & ~15) + lane
             for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
                 const int st = it % ST;
                 const int64_t m0 = (int64_t)j * kBN;
                 if (j == g.tile0 || (j & 15) == 0) {
                     const int64_t slot = ((int64_t)(j & ~15) * 2 + lane) * 64;
-                    page = slot < end ? page_of(a.pk, g.b, slot, a.status) : -1;
+                    page = slot + 64 > (int64_t)g.tile0 * kBN && slot < end ? page_of(a.pk, g.b, slot, a.status) : -1;
                 }
-                const int pg0 = __shfl_sync(0xffffffffu, page, (j & 15) * 2);
-                const int pg1 = __shfl_sync(0xffffffffu, page, (j & 15) * 2 + 1);
-                // The tile's band.  Over prefix tiles both distances shrink, so the bounds only
-                // move down; a tile with nodes may hold any small distance.
-                if (m0 + kBN <= g.L) {
-                    const int64_t dmin = pmin - (m0 + kBN - 1), dmax = pmax - m0;
-                    if (j == g.tile0) {
-                        r_lo = first_kept(w, H, dmin);
-                        r_full = first_kept(w, H, dmax);
-                    }
-                    while (r_lo > 0 && (int64_t)w[r_lo - 1] >= dmin) --r_lo;
-                    while (r_full > 0 && (int64_t)w[r_full - 1] >= dmax) --r_full;
-                } else {
-                    r_lo = 0;
-                    r_full = first_kept(w, H, pmax - (m0 < g.L && m0 < kmin ? m0 : kmin));
-                }
-                wc.site = 41;
-                if (!(ok = mbar_wait_warp(&ctl->k_empty[st], ((it / ST) & 1) ^ 1, wc))) break;
+                const int pg = __shfl_sync(0xffffffffu, page, (j & 15) * 2 + (box_keys == kBN ? 0 : hf));
                 const int halves = box_keys == kBN || m0 + 64 < end ? 2 : 1;
-                const int ca = r_lo >> 3;
-                if (lane == 0) {
-                    ctl->band[st][0] = r_lo;
-                    ctl->band[st][1] = r_full;
-                    const uint32_t bytes = kPacked ? (uint32_t)(C - ca) * 2048u * halves : (uint32_t)(D / 64) * 8192u * halves;
-                    mbar_expect_tx(&ctl->k_full[st], bytes);
-                }
-                __syncwarp();
-                last[st] = it;
-                const int at = (int)(m0 % a.pk.page_size);
-                const int hf = lane & 1, u = lane >> 1;  // lane = (K-step or dim group, half)
-                const int pg = hf ? pg1 : pg0;
-                const int hat = box_keys == kBN ? at : (int)((m0 + 64 * hf) % a.pk.page_size);
                 const bool issue = hf < (box_keys == kBN ? 1 : halves);
-                uint8_t *kst = sK + st * F::TileBytes, *vst = sV + st * F::TileBytes;
-                if constexpr (kPacked) {
-                    if (issue && u >= ca && u < C)
-                        tma_load_3d(kst + u * 4096 + hf * 2048, &tm_k, &ctl->k_full[st], 0, hat, (pg * sh.Hkv + g.h) * C + u);
-                } else {
-                    if (issue && u < D / 64)
-                        tma_load_4d(kst + u * 16384 + hf * 8192, &tm_k, &ctl->k_full[st], 64 * u, g.h, hat, pg);
+                const int at = (int)(((uint32_t)m0 + 64u * hf) % P);
+                if (!v) {
+                    // The tile's band.  Over prefix tiles both distances shrink, so the bounds only
+                    // move down; a tile with nodes may hold any small distance.
+                    if (m0 + kBN <= g.L) {
+                        const int64_t dmin = g.pmin - (m0 + kBN - 1), dmax = g.pmax - m0;
+                        if (j == g.tile0) {
+                            r_lo = first_kept(w, H, dmin);
+                            r_full = first_kept(w, H, dmax);
+                        }
+                        while (r_lo > 0 && (int64_t)w[r_lo - 1] >= dmin) --r_lo;
+                        while (r_full > 0 && (int64_t)w[r_full - 1] >= dmax) --r_full;
+                    } else {
+                        r_lo = 0;
+                        r_full = first_kept(w, H, g.pmax - (m0 < g.L ? min(m0, (int64_t)g.kmin) : (int64_t)g.kmin));
+                    }
                 }
-                wc.site = 42;
-                if (!(ok = mbar_wait_warp(&ctl->v_empty[st], ((it / ST) & 1) ^ 1, wc))) break;
-                if (lane == 0) mbar_expect_tx(&ctl->v_full[st], (uint32_t)(D / 64) * 8192u * halves);
+                if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
+                const int ca = v || !kPacked ? 0 : r_lo >> 3;
+                if (lane == 0) {
+                    if (!v) {
+                        ctl->band[st][0] = r_lo;
+                        ctl->band[st][1] = r_full;
+                    }
+                    mbar_expect_tx(&full[st], (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves);
+                }
                 __syncwarp();
-                lastv = it;
-                if (issue && u < D / 64)
-                    tma_load_4d(vst + u * 16384 + hf * 8192, &tm_v, &ctl->v_full[st], 64 * u, g.h, hat, pg);
+                uint8_t *dst = (v ? sV : sK) + st * F::TileBytes;
+                if (kPacked && !v) {
+                    if (issue && u >= ca && u < C)
+                        tma_load_3d(dst + u * 4096 + hf * 2048, &tm_k, &full[st], 0, at, (pg * sh.Hkv + g.h) * C + u);
+                } else if (issue && u < D / 64) {
+                    tma_load_4d(dst + u * 16384 + hf * 8192, v ? &tm_v : &tm_k, &full[st], 64 * u, g.h, at, pg);
+                }
             }
         }
         if (!ok) {
-            // Let every copy land before the CTA exits.
-            const uint64_t drain_ns = atflash_drain_limit_ns(a.limit_ns);
-            for (int s = 0; s < ST; ++s)
-                if (last[s] >= 0) {
-                    wait_drain(&ctl->k_full[s], (last[s] / ST) & 1, drain_ns);
-                    const int v = last[s] <= lastv ? last[s] : last[s] - ST;
-                    if (v >= 0) wait_drain(&ctl->v_full[s], (v / ST) & 1, drain_ns);
-                }
+            // Let every copy land before the CTA exits: the tiles before `it` are issued.
+            for (int x = it > ST ? it - ST : 0; x < it; ++x)
+                wait_drain(&full[x % ST], (x / ST) & 1, atflash_drain_limit_ns(a.limit_ns));
         }
     } else if (warp == kFix) {
-        // ------------------------------------- boundary pairs of K, tail of V
-        for (; ok && walk.next(a, sh, member, g); ++seg) {
-            const int64_t end = g.L + g.nodes;
+        // ------------------------------------------------ boundary pairs of K
+        while (ok && runs.next(wc, ok)) {
+            const Segment g = runs.now();
+            runs.done(lane);
+            const int64_t end = (int64_t)g.L + g.nodes;
             for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
                 const int st = it % ST;
                 const int64_t m0 = (int64_t)j * kBN;
-                wc.site = 43;
-                if (!(ok = mbar_wait_warp(&ctl->k_full[st], (it / ST) & 1, wc))) break;
+                if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
                 const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
+                if (!needs_fix<kPacked>(r_lo, r_full)) continue;
                 uint8_t *kst = sK + st * F::TileBytes;
                 if (r_lo < r_full) {
                     int *kp = sKpos + st * kBN;
                     for (int e = lane; e < kBN; e += 32) {
                         const int64_t slot = m0 + e;
-                        kp[e] = slot < g.L || slot >= end ? (int)slot : (int)node_pos(a, g, (int)(slot - g.L));
+                        kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
                     }
                     const int rs = max(r_lo, r_full - kStaged), nb = r_full - rs;
                     uint32_t *sw = sStage + st * (kStaged * kBN);
@@ -448,70 +511,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 // Pairs of the first K-step of the MMA that are not kept by every cell.
-                constexpr int kPer = kPacked ? 8 : 16;
                 const int z0 = r_full / kPer * kPer;
-                if (r_full > z0 && r_full <= H) {
+                if (r_full > z0) {
                     const int nz = r_full - z0;
                     for (int e = lane; e < nz * kBN; e += 32) store_pair<D, kPacked>(kst, e & (kBN - 1), z0 + (e >> 7), 0u);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
-                if (m0 + kBN > g.L) {
-                    // V behind the last node may hold anything (0 * NaN must not reach O), and so
-                    // may a node that some rows do not see: its non-finite values are taken out
-                    // here and put back for the rows that see them at the end of the segment.
-                    wc.site = 44;
-                    if (!(ok = mbar_wait_warp(&ctl->v_full[st], (it / ST) & 1, wc))) break;
-                    uint8_t *vst = sV + st * F::TileBytes;
-                    constexpr int kUnits = D / 8;  // 16-byte units of a row
-                    bool bad = false;
-                    const int first = (int)max(g.L - m0, (int64_t)0);
-                    for (int e = first * kUnits + lane; e < kBN * kUnits; e += 32) {
-                        const int row = e / kUnits, d = e % kUnits * 8;
-                        uint4 *p = reinterpret_cast<uint4 *>(vst + sw128_off(row, d));
-                        if (m0 + row >= end) {
-                            *p = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 x = *p;
-                        uint32_t *xs = reinterpret_cast<uint32_t *>(&x);
-                        bool odd = false;
+            }
+        }
+    } else if (warp >= kTail) {
+        // ---------------- tiles with nodes: mask bits, V behind the last node
+        const int t2 = warp - kTail;
+        uint32_t used = 0;  // phase bit of each set's mask buffer
+        while (ok && runs.next(wc, ok)) {
+            const Segment g = runs.now();
+            runs.done(lane);
+            const int seg = runs.n - 1;
+            const int64_t end = (int64_t)g.L + g.nodes;
+            const int i0 = g.row0 / sh.G, i1 = (g.row0 + g.rows - 1) / sh.G;
+            for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
+                const int st = it % ST, set = it & 1;
+                const int64_t m0 = (int64_t)j * kBN;
+                if (m0 + kBN <= g.L) continue;
+                // One mask buffer per set.
+                if (!(ok = wait(&ctl->m_empty[set], ((used >> set) & 1) ^ 1, wc, 44))) break;
+                used ^= 1u << set;
+                for (int i = i0 + t2; i <= i1; i += 4) {
+                    uint32_t x[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((xs[i] & 0x7F80u) == 0x7F80u) xs[i] &= 0xFFFF0000u, odd = true;
-                            if ((xs[i] & 0x7F800000u) == 0x7F800000u) xs[i] &= 0x0000FFFFu, odd = true;
-                        }
-                        if (odd) *p = x;
-                        bad |= odd;
+                    for (int e = 0; e < 8; ++e) {
+                        const int i2 = i + 2 * (e >> 2);
+                        const int64_t slot = m0 + 32 * (e & 3) + lane;
+                        const bool sees = i2 <= i1 && slot < end && (slot < g.L || node_sees(a, g.b, i2, (int)(slot - g.L)));
+                        x[e] = __ballot_sync(0xffffffffu, sees);
                     }
-                    if (__any_sync(0xffffffffu, bad) && lane == 0) ctl->nf_seg[seg & 7] = seg;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->v_ready[st]);
+                    if (lane == 0) {
+                        sMask[set * kBM + i - i0] = make_uint4(x[0], x[1], x[2], x[3]);
+                        if (i + 2 <= i1) sMask[set * kBM + i + 2 - i0] = make_uint4(x[4], x[5], x[6], x[7]);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->m_full[set]);
+                // V behind the last node may hold anything (0 * NaN must not reach O), and so may
+                // a node that some rows do not see: its non-finite values are taken out here and
+                // put back, for the rows that see them, at the end of the run.
+                if (!(ok = wait(&ctl->v_full[st], (it / ST) & 1, wc, 45))) break;
+                uint8_t *vst = sV + st * F::TileBytes;
+                constexpr int kUnits = D / 8;  // 16-byte units of a row
+                bool bad = false;
+                const int first = (int)max(g.L - m0, (int64_t)0);
+                for (int e = first * kUnits + t2 * 32 + lane; e < kBN * kUnits; e += 64) {
+                    const int row = e / kUnits, d = e % kUnits * 8;
+                    uint4 *p = reinterpret_cast<uint4 *>(vst + sw128_off(row, d));
+                    if (m0 + row >= end) {
+                        *p = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 x = *p;
+                    uint32_t *xs = reinterpret_cast<uint32_t *>(&x);
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((xs[i] & 0x7F80u) == 0x7F80u) xs[i] &= 0xFFFF0000u, odd = true;
+                        if ((xs[i] & 0x7F800000u) == 0x7F800000u) xs[i] &= 0x0000FFFFu, odd = true;
+                    }
+                    if (odd) *p = x;
+                    bad |= odd;
+                }
+                if (__any_sync(0xffffffffu, bad) && lane == 0) ctl->nf_seg[seg & 7] = seg;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->v_ready[st]);
             }
         }
     } else if (warp == kQk) {
         // ------------------------------------------------------- QK issuer
         const uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
         const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
-        constexpr int kPer = kPacked ? 8 : 16, kSteps = H / kPer;
-        for (; ok && walk.next(a, sh, member, g); ++seg) {
-            wc.site = 45;
-            if (!(ok = mbar_wait_warp(&ctl->q_ready, seg & 1, wc))) break;
-            for (int j = 0; ok && j < g.ntile; ++j, ++it) {
-                const int st = it % ST, buf = it & 1;
-                wc.site = 46;
-                if (!(ok = mbar_wait_warp(&ctl->k_ready[st], (it / ST) & 1, wc))) break;
-                const int c0 = ctl->band[st][1] / kPer;
-                wc.site = 47;
-                if (it >= 2 && !(ok = mbar_wait_warp(&ctl->s_read[buf], ((it >> 1) - 1) & 1, wc))) break;
+        uint32_t fixed = 0;  // phase bit of k_ready per stage
+        while (ok && runs.next(wc, ok)) {
+            const int ntile = runs.now().ntile;
+            runs.done(lane);
+            if (!(ok = wait(&ctl->q_ready, (runs.n - 1) & 1, wc, 46))) break;
+            for (int j = 0; ok && j < ntile; ++j, ++it) {
+                const int st = it % ST, set = it & 1;
+                if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
+                const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
+                if (needs_fix<kPacked>(r_lo, r_full)) {
+                    if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
+                    fixed ^= 1u << st;
+                }
+                // S of this set is free once it has been read, or, with P over it, once P has.
+                if (it >= 2 && !(ok = wait(F::PoverS ? &ctl->o_done[set] : &ctl->s_read[set], ((it >> 1) - 1) & 1, wc, 49))) break;
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + F::TmemS + buf * kBN;
+                    const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + set * kBN;
                     uint32_t acc = 0;
-                    for (int c = c0; c < kSteps; ++c) {
+                    for (int c = r_full / kPer; c < H / kPer; ++c) {
 #pragma unroll
                         for (int part = 0; part < (kPacked ? 1 : 2); ++part) {
                             // Packed: one K-step is 8 whole pairs.  Natural: 16 dims of the low half,
@@ -528,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    umma_commit(&ctl->s_full[buf]);
+                    umma_commit(&ctl->s_full[set]);
                     umma_commit(&ctl->k_empty[st]);
                 }
                 __syncwarp();
@@ -539,336 +637,435 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_bf16_f32(kBM, D, false, true);
         const uint32_t sVa = smem_u32(sV);
         uint32_t tails = 0;  // phase bit of v_ready per stage
-        for (; ok && walk.next(a, sh, member, g); ++seg) {
-            for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
-                const int st = it % ST, buf = it & 1;
-                wc.site = 48;
-                if (!(ok = mbar_wait_warp(&ctl->v_full[st], (it / ST) & 1, wc))) break;
-                if ((int64_t)(j + 1) * kBN > g.L) {
-                    wc.site = 49;
-                    if (!(ok = mbar_wait_warp(&ctl->v_ready[st], (tails >> st) & 1, wc))) break;
+        while (ok && runs.next(wc, ok)) {
+            const int L = runs.now().L, tile0 = runs.now().tile0, ntile = runs.now().ntile;
+            runs.done(lane);
+            for (int j = tile0; ok && j < tile0 + ntile; ++j, ++it) {
+                const int st = it % ST, set = it & 1;
+                if (!(ok = wait(&ctl->v_full[st], (it / ST) & 1, wc, 50))) break;
+                if ((int64_t)(j + 1) * kBN > L) {
+                    if (!(ok = wait(&ctl->v_ready[st], (tails >> st) & 1, wc, 51))) break;
                     tails ^= 1u << st;
                 }
-                wc.site = 50;
-                if (!(ok = mbar_wait_warp(&ctl->p_full[buf], (it >> 1) & 1, wc))) break;
+                if (!(ok = wait(&ctl->p_full[set], (it >> 1) & 1, wc, 52))) break;
                 if (lane == 0) {
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk) {
                         const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
-                        umma_bf16_ts(tmem + F::TmemO, tmem + F::TmemP + buf * 64 + kk * 8, db, idesc, (j > g.tile0 || kk > 0) ? 1u : 0u);
+                        umma_bf16_ts(tmem + F::TmemO + set * D, tmem + F::TmemP + set * F::TmemPStep + kk * 8, db, idesc,
+                                     (j >= tile0 + 2 || kk > 0) ? 1u : 0u);
                     }
-                    umma_commit(&ctl->o_done[buf]);
+                    umma_commit(&ctl->o_done[set]);
                     umma_commit(&ctl->v_empty[st]);
                 }
                 __syncwarp();
             }
         }
-    } else {
+    } else if (warp < kSoft) {
         // ------------------------------------------------------------- softmax
         setmaxnreg_inc<kSoftRegs>();
-        const int q4 = warp & 3, hc = warp >> 2;
-        const int c0 = 64 * hc;
-        constexpr int kO = D / 2;  // O columns of this warp
+        const int set = warp >> 2, q4 = warp & 3;
+        const int copy = q4 * 32 / kRows;                // which copy of the rows, hence which columns
+        const int c0 = copy * NC;
+        const int row = (q4 * 32) % kRows + lane;        // row of the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const uint32_t tS = tmem + F::TmemS + lane_off + c0, tP = tmem + F::TmemP + lane_off + c0 / 2;
-        const uint32_t tO = tmem + F::TmemO + lane_off + hc * kO;
+        const uint32_t tS = tmem + set * kBN + lane_off;
+        const uint32_t tP = tmem + F::TmemP + set * F::TmemPStep + lane_off;
+        const uint32_t tO = tmem + F::TmemO + set * D + lane_off;
         const float scale_log2 = 1.4426950408889634f * rsqrtf((float)D);
-        int nx = 0, nl = 0;  // exchanges with the row's other warp
-        for (; ok && walk.next(a, sh, member, g); ++seg) {
-            const bool live = q4 * 32 < g.rows;  // some row of this quarter exists
-            const int row = q4 * 32 + lane;
-            const bool valid = row < g.rows;
-            const int tok = valid ? (g.row0 + row) / sh.G : 0, head = valid ? (g.row0 + row) % sh.G : 0;
-            const int64_t pos = valid ? node_pos(a, g, tok) : 0;
-            const int64_t end = g.L + g.nodes;
-            if (live) {
-                // Rotate this quarter's queries into the MMA's layout (this warp: half of the
-                // pairs of each row) as hi + lo bf16.  The previous segment's MMAs have read
-                // their Q (its last S was waited for), the row's other warp too (it has posted
-                // its sum).
-                constexpr int kLP = H / 2, kRows = 32 / kLP;  // lanes per row, rows at a time
-                const int pr = hc * kLP + lane % kLP;
-                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + g.b * a.qs.batch;
-                int last_tok = -1;
+        uint32_t fixed = 0;                              // phase bit of k_ready per stage
+        int syncs = 0, tails = 0;
+        // All softmax warps (bounded, unlike a named barrier).
+        auto soft_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->soft_bar);
+            return wait(&ctl->soft_bar, syncs++ & 1, wc, 53);
+        };
+        uint32_t zero[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0;
+        if (!F::PoverS && kRep > 1) {
+            // P is zero in the other copies' columns for good.
+#pragma unroll
+            for (int i = 0; i < kRep; ++i)
+                if (i != copy)
+                    for (int x = 0; x < NC / 32; ++x) tmem_st_x16(tP + i * (NC / 2) + 16 * x, zero);
+            tmem_st_wait();
+        }
+        while (ok && runs.next(wc, ok)) {
+            const Segment &g = runs.now();
+            const int rows = g.rows, row0 = g.row0, b = g.b, L = g.L, tile0 = g.tile0, ntile = g.ntile;
+            const bool live = (q4 * 32) % kRows < rows;  // some row of this warp exists
+            const bool valid = row < rows;
+            const int tok = (row0 + (valid ? row : 0)) / sh.G;
+            {
+                // Rotate the queries into the MMA's layout as hi + lo bf16: a thread takes one pair
+                // of every kStep-th row, so neighbouring rows (heads) of a node share its cos and sin.
+                constexpr int kStep = 256 / H;
+                const int pr = threadIdx.x % H;
+                int r = threadIdx.x / H;
+                int t = (row0 + r) / sh.G, hh = (row0 + r) % sh.G, last = -1;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + b * a.qs.batch + (int64_t)g.h * sh.G * a.qs.head + pr;
                 float2 cs = make_float2(1.f, 0.f);
 #pragma unroll 1
-                for (int r8 = 0; r8 < 32; r8 += 8 * kRows) {
-                    __nv_bfloat16 xa[8], xb[8];
+                for (; r < rows; r += 4 * kStep) {
+                    __nv_bfloat16 xa[4], xb[4];
+                    int ts[4];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int rr = q4 * 32 + r8 + u * kRows + lane / kLP;
-                        xa[u] = xb[u] = __float2bfloat16_rn(0.f);
-                        if (rr < g.rows) {
-                            const int t = (g.row0 + rr) / sh.G, hh = g.h * sh.G + (g.row0 + rr) % sh.G;
+                    for (int u = 0; u < 4; ++u) {
+                        ts[u] = t;
+                        if (r + u * kStep < rows) {
                             const __nv_bfloat16 *src = q + t * a.qs.token + hh * a.qs.head;
-                            xa[u] = src[pr];
-                            xb[u] = src[pr + H];
+                            xa[u] = src[0];
+                            xb[u] = src[H];
                         }
+                        hh += kStep;
+                        while (hh >= sh.G) hh -= sh.G, ++t;
                     }
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int rr = q4 * 32 + r8 + u * kRows + lane / kLP;
-                        const int t = min(g.row0 + rr, g.row0 + g.rows - 1) / sh.G;
-                        if (t != last_tok) {
-                            cs = turn_cos_sin((int32_t)node_pos(a, g, t), rt.turn[pr]);
-                            last_tok = t;
+                    for (int u = 0; u < 4; ++u) {
+                        const int rr = r + u * kStep;
+                        if (rr >= rows) break;
+                        if (ts[u] != last) {
+                            last = ts[u];
+                            cs = turn_cos_sin(node_pos(a, b, L, last), rt.turn[pr]);
                         }
                         const float fa = __bfloat162float(xa[u]), fb = __bfloat162float(xb[u]);
                         const float x = fa * cs.x - fb * cs.y, y = fb * cs.x + fa * cs.y;
                         const uint32_t hi = pack_bf16x2(x, y);
                         const uint32_t lo = pack_bf16x2(x - bf16lo(hi), y - bf16hi(hi));
-                        store_pair<D, kPacked>(sQ, rr, pr, hi);
-                        store_pair<D, kPacked>(sQ + F::TileBytes, rr, pr, lo);
+#pragma unroll
+                        for (int cp = 0; cp < kRep; ++cp) {
+                            store_pair<D, kPacked>(sQ, cp * kRows + rr, pr, hi);
+                            store_pair<D, kPacked>(sQ + F::TileBytes, cp * kRows + rr, pr, lo);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->q_ready);
-            wc.site = 51;
-            if (!(ok = mbar_wait_warp(&ctl->q_ready, seg & 1, wc))) break;  // the other warp's half, for the boundary pairs
+            const int pos = valid ? node_pos(a, b, L, tok) : 0;
+            if (!(ok = wait(&ctl->q_ready, (runs.n - 1) & 1, wc, 54))) break;  // the other warps' pairs, for the boundary
 
             float m_used = -INFINITY, lrun = 0.f;
-            for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
-                const int st = it % ST, buf = it & 1;
-                const int64_t m0 = (int64_t)j * kBN;
-                const bool tail = m0 + kBN > g.L;
-                uint32_t see0 = 0xffffffffu, see1 = 0xffffffffu;  // this row's columns c0.., c0 + 32..
-                if (tail && live) {
-                    // Columns 32 c.. of every node of this quarter's rows, by ballot.
-                    const int64_t s0 = m0 + c0 + lane, s1 = s0 + 32;
-                    const int ta = (g.row0 + q4 * 32) / sh.G, tb = (g.row0 + min(q4 * 32 + 31, g.rows - 1)) / sh.G;
-                    see0 = see1 = 0;
-                    for (int t = ta; t <= tb; ++t) {
-                        const bool v0 = s0 < end && (s0 < g.L || node_sees(a, g, t, (int)(s0 - g.L)));
-                        const bool v1 = s1 < end && (s1 < g.L || node_sees(a, g, t, (int)(s1 - g.L)));
-                        const uint32_t b0 = __ballot_sync(0xffffffffu, v0), b1 = __ballot_sync(0xffffffffu, v1);
-                        if (t == tok) see0 = b0, see1 = b1;
-                    }
-                }
-                wc.site = 52;
-                if (!(ok = mbar_wait_warp(&ctl->k_ready[st], (it / ST) & 1, wc))) break;
+            const int j0 = tile0 + ((it ^ set) & 1);  // this set's tiles
+            for (int j = j0; j < tile0 + ntile; j += 2) {
+                const int x = it + (j - tile0), st = x % ST;
+                if (!(ok = wait(&ctl->k_full[st], (x / ST) & 1, wc, 55))) break;
                 const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
-                wc.site = 53;
-                if (!(ok = mbar_wait_warp(&ctl->s_full[buf], (it >> 1) & 1, wc))) break;
+                const bool fix = needs_fix<kPacked>(r_lo, r_full), boundary = r_lo < r_full;
+                const bool tail = (int64_t)(j + 1) * kBN > L;
+                __syncwarp();
+                if (!boundary && lane == 0) mbar_arrive(&ctl->k_empty[st]);  // nothing else of K is read here
+                if (!(ok = wait(&ctl->s_full[set], (x >> 1) & 1, wc, 56))) break;
                 tc_fence_after();
-                float s[64];
-                if (live) {
+                if (fix) {
+                    // Waited for only where this warp still holds the stage (boundary pairs), so that
+                    // the barrier cannot be a phase ahead of it.
+                    if (boundary && !(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 57))) break;
+                    fixed ^= 1u << st;
+                }
+                if (tail) {
+                    if (!(ok = wait(&ctl->m_full[set], tails & 1, wc, 58))) break;
+                    ++tails;
+                }
+                // The row's maximum, CW columns at a time, the first ones last: they stay in
+                // registers for the exponentials (128 columns at once would spill); the others are
+                // read again, after having been written back where the tensor core's scores were
+                // not the last word.
+                float s[CW], mx = -INFINITY;
+#pragma unroll 1
+                for (int part = NC / CW - 1; part >= 0 && live; --part) {
+                    const int cc = c0 + part * CW;
                     if (r_full < H) {
-                        uint32_t ra[64];
-                        tmem_ld_32x32b_x64(tS + buf * kBN, ra);
+                        uint32_t ra[CW];
+                        if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + cc, ra);
+                        else tmem_ld_32x32b_x32(tS + cc, ra);
                         tmem_ld_wait(ra);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(ra[i]);
+                        for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = 0.f;
+                        for (int i = 0; i < CW; ++i) s[i] = 0.f;
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->s_read[buf]);
-                if (live && r_lo < r_full) {
-                    const uint8_t *kst = sK + st * F::TileBytes;
-                    const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + c0);
-                    const int rs = max(r_lo, r_full - kStaged);
-                    for (int r = r_lo; r < r_full; ++r) {
-                        // Keys at positions >= lim keep the pair.
-                        const int64_t l64 = pos - (int64_t)w[r];
-                        const int lim = !valid || l64 > INT32_MAX ? INT32_MAX : (l64 < INT32_MIN ? INT32_MIN : (int)l64);
-                        const uint32_t qh = load_pair<D, kPacked>(sQ, row, r), ql = load_pair<D, kPacked>(sQ + F::TileBytes, row, r);
-                        const float qa = bf16lo(qh) + bf16lo(ql), qb = bf16hi(qh) + bf16hi(ql);
-                        auto add4 = [&](int i, uint4 k) {
-                            const int4 p = kp[i];
-                            s[4 * i] += p.x >= lim ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
-                            s[4 * i + 1] += p.y >= lim ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
-                            s[4 * i + 2] += p.z >= lim ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
-                            s[4 * i + 3] += p.w >= lim ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
-                        };
-                        if (r >= rs) {
-                            const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + st * (kStaged * kBN) + (r - rs) * kBN + c0);
+                    if (boundary) {
+                        const uint8_t *kst = sK + st * F::TileBytes;
+                        const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + cc);
+                        const int rs = max(r_lo, r_full - kStaged);
+#pragma unroll 1
+                        for (int r = r_lo; r < r_full; ++r) {
+                            // Keys at positions >= lim keep the pair.
+                            const int64_t l64 = (int64_t)pos - w[r];
+                            const int lim = !valid ? INT32_MAX : (l64 < INT32_MIN ? INT32_MIN : (int)l64);
+                            const uint32_t qh = load_pair<D, kPacked>(sQ, copy * kRows + row, r);
+                            const uint32_t ql = load_pair<D, kPacked>(sQ + F::TileBytes, copy * kRows + row, r);
+                            const float qa = bf16lo(qh) + bf16lo(ql), qb = bf16hi(qh) + bf16hi(ql);
+                            auto add4 = [&](int i, uint4 k) {
+                                const int4 p = kp[i];
+                                s[4 * i] += p.x >= lim ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
+                                s[4 * i + 1] += p.y >= lim ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
+                                s[4 * i + 2] += p.z >= lim ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
+                                s[4 * i + 3] += p.w >= lim ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
+                            };
+                            if (r >= rs) {
+                                const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + st * (kStaged * kBN) + (r - rs) * kBN + cc);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) add4(i, kw[i]);
-                        } else {
-                            // More boundary pairs than staged: those below are whole in the K tile.
+                                for (int i = 0; i < CW / 4; ++i) add4(i, kw[i]);
+                            } else {
+                                // More boundary pairs than staged: those below are whole in the K tile.
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                uint4 k;
-                                k.x = load_pair<D, kPacked>(kst, c0 + 4 * i, r);
-                                k.y = load_pair<D, kPacked>(kst, c0 + 4 * i + 1, r);
-                                k.z = load_pair<D, kPacked>(kst, c0 + 4 * i + 2, r);
-                                k.w = load_pair<D, kPacked>(kst, c0 + 4 * i + 3, r);
-                                add4(i, k);
+                                for (int i = 0; i < CW / 4; ++i) {
+                                    uint4 k;
+                                    k.x = load_pair<D, kPacked>(kst, cc + 4 * i, r);
+                                    k.y = load_pair<D, kPacked>(kst, cc + 4 * i + 1, r);
+                                    k.z = load_pair<D, kPacked>(kst, cc + 4 * i + 2, r);
+                                    k.w = load_pair<D, kPacked>(kst, cc + 4 * i + 3, r);
+                                    add4(i, k);
+                                }
                             }
                         }
                     }
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(&ctl->k_empty[st]);
-                float alpha = 1.f;
-                bool need = false;
-                uint32_t pk[32];
-                float psum = 0.f;
-                if (live) {
                     if (tail) {
+                        const uint32_t *mask = reinterpret_cast<const uint32_t *>(sMask + set * kBM + (tok - row0 / sh.G)) + cc / 32;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (!((see0 >> i) & 1u)) s[i] = -INFINITY;
-                            if (!((see1 >> i) & 1u)) s[32 + i] = -INFINITY;
+                        for (int i = 0; i < CW / 32; ++i) {
+                            const uint32_t see = mask[i];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
                         }
                     }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8) {
-                        mx0 = max3(mx0, s[i], s[i + 1]);
-                        mx1 = max3(mx1, s[i + 2], s[i + 3]);
-                        mx2 = max3(mx2, s[i + 4], s[i + 5]);
-                        mx3 = max3(mx3, s[i + 6], s[i + 7]);
+                    for (int i = 0; i < CW; i += 8) {
+                        mx = max3(mx, s[i], s[i + 1]);
+                        mx0 = max3(mx0, s[i + 2], s[i + 3]);
+                        mx1 = max3(mx1, s[i + 4], s[i + 5]);
+                        mx2 = max3(mx2, s[i + 6], s[i + 7]);
                     }
-                    float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                    // The row's maximum over both column halves (a slot of this parity is rewritten
-                    // only after the partner has passed the next exchange).
-                    float *slot = ctl->xval[q4][nx & 1][0];
-                    slot[hc * 32 + lane] = mx;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->xbar[q4]);
-                    wc.site = 54;
-                    if (!(ok = mbar_wait_warp(&ctl->xbar[q4], nx & 1, wc))) break;
-                    mx = fmaxf(mx, slot[(hc ^ 1) * 32 + lane]);
-                    ++nx;
-                    // The running max is kept unless it grew by more than 2^8: O / l uses the same
-                    // one, so the result does not depend on it.
-                    const float tile_max = mx * scale_log2;
-                    need = tile_max > m_used + kRescaleThreshold;
-                    const float m_new = need ? tile_max : m_used;
-                    alpha = need ? fast_exp2(m_used - m_new) : 1.f;
-                    m_used = m_new;
-                    const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen so far
-                    const float2 mneg = make_float2(-mr, -mr), sc2 = make_float2(scale_log2, scale_log2);
-                    float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
+                    mx = fmaxf(fmaxf(mx, mx0), fmaxf(mx1, mx2));
+                    if (part > 0 && (boundary || tail || r_full >= H)) {
+                        __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float2 xa = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mneg);
-                        float2 xb = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), sc2, mneg);
-                        xa.x = fast_exp2(xa.x);
-                        xa.y = fast_exp2(xa.y);
-                        xb.x = fast_exp2(xb.x);
-                        xb.y = fast_exp2(xb.y);
-                        l0 = add2(l0, xa);
-                        l1 = add2(l1, xb);
-                        pk[i] = pack_bf16x2(xa.x, xa.y);
-                        pk[i + 1] = pack_bf16x2(xb.x, xb.y);
+                        for (int i = 0; i < CW; i += 32) tmem_st_32x32b_x32(tS + cc + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
+                        tmem_st_wait();
                     }
-                    const float2 ls = add2(l0, l1);
-                    psum = ls.x + ls.y;
                 }
-                // P of this parity is free once PV(it - 2) is done (every warp waits, also one
-                // without rows: its arrivals must not run ahead of the others').
-                if (it >= 2) {
-                    wc.site = 55;
-                    if (!(ok = mbar_wait_warp(&ctl->o_done[buf], ((it >> 1) - 1) & 1, wc))) break;
-                    tc_fence_after();
-                }
-                if (live) {
-                    if (j > g.tile0 && __any_sync(0xffffffffu, need)) {
-                        // O may be rescaled once PV(it - 1) is done.
-                        wc.site = 56;
-                        if (!(ok = mbar_wait_warp(&ctl->o_done[buf ^ 1], ((it - 1) >> 1) & 1, wc))) break;
-                        tc_fence_after();
+                __syncwarp();
+                if (boundary && lane == 0) mbar_arrive(&ctl->k_empty[st]);
+                if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
+                // The running max is kept unless it grew by more than 2^8: O / l uses the same one,
+                // so the result does not depend on it.
+                const float tile_max = mx * scale_log2;
+                const bool need = live && tile_max > m_used + kRescaleThreshold;
+                const float m_new = need ? tile_max : m_used;
+                const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+                m_used = m_new;
+                const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen so far
+                const float2 mneg = make_float2(-mr, -mr), sc2 = make_float2(scale_log2, scale_log2);
+                float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-                        for (int cc = 0; cc < kO / 32; ++cc) {
-                            uint32_t r[32];
-                            tmem_ld_32x32b_x32(tO + cc * 32, r);
-                            tmem_ld_wait(r);
+                for (int part = 0; part < NC / CW; ++part) {
+                    uint32_t pk[CW / 2];
+                    if (live) {
+                        if (part > 0) {
+                            uint32_t ra[CW];
+                            if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + c0 + part * CW, ra);
+                            else tmem_ld_32x32b_x32(tS + c0 + part * CW, ra);
+                            tmem_ld_wait(ra);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                            tmem_st_32x32b_x32(tO + cc * 32, r);
+                            for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < CW / 2; i += 2) {
+                            float2 xa = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mneg);
+                            float2 xb = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), sc2, mneg);
+                            xa.x = fast_exp2(xa.x);
+                            xa.y = fast_exp2(xa.y);
+                            xb.x = fast_exp2(xb.x);
+                            xb.y = fast_exp2(xb.y);
+                            l0 = add2(l0, xa);
+                            l1 = add2(l1, xb);
+                            pk[i] = pack_bf16x2(xa.x, xa.y);
+                            pk[i + 1] = pack_bf16x2(xb.x, xb.y);
                         }
                     }
-                    tmem_st_32x32b_x32(tP + buf * 64, pk);
+                    if (part == NC / CW - 1 && !F::PoverS) {
+                        // S has been read.
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->s_read[set]);
+                    }
+                    // P and O of this set are free once its previous PV is done (with P over S, this
+                    // tile's QK has waited for that).  Every warp waits, also one without rows: its
+                    // arrivals must not run ahead of the others'.
+                    if (part == 0) {
+                        if (!F::PoverS && x >= 2) {
+                            if (!(ok = wait(&ctl->o_done[set], ((x >> 1) - 1) & 1, wc, 61))) break;
+                            tc_fence_after();
+                        }
+                        if (j >= tile0 + 2 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                            for (int cc = 0; cc < D / 32; ++cc) {
+                                uint32_t r[32];
+                                tmem_ld_32x32b_x32(tO + cc * 32, r);
+                                tmem_ld_wait(r);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                                tmem_st_32x32b_x32(tO + cc * 32, r);
+                            }
+                        }
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < CW / 32; ++i) tmem_st_x16(tP + (c0 + part * CW) / 2 + 16 * i, pk + 16 * i);
+                    }
+                }
+                if (!ok) break;
+                if (live) {
+                    if (F::PoverS && kRep > 1) {
+#pragma unroll
+                        for (int i = 0; i < kRep; ++i)
+                            if (i != copy) {
+#pragma unroll
+                                for (int y = 0; y < NC / 32; ++y) tmem_st_x16(tP + i * (NC / 2) + 16 * y, zero);
+                            }
+                    }
                     tmem_st_wait();
-                    lrun = lrun * alpha + psum;
+                    const float2 ls = add2(l0, l1);
+                    lrun = lrun * alpha + (ls.x + ls.y);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->p_full[buf]);
+                if (lane == 0) mbar_arrive(&ctl->p_full[set]);
             }
             if (!ok) break;
-            if (!live) continue;
-            // The row's sum over both column halves, then O.
-            ctl->lval[q4][hc][lane] = lrun;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->lbar[q4]);
-            wc.site = 57;
-            if (!(ok = mbar_wait_warp(&ctl->lbar[q4], nl & 1, wc))) break;
-            ++nl;
-            lrun += ctl->lval[q4][hc ^ 1][lane];
-            wc.site = 58;
-            if (!(ok = mbar_wait_warp(&ctl->o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, wc))) break;
+            it += ntile;
+            // ---- end of the run: the sets' (and copies') states of each row joined
+            const int lastx = it - 1 - ((it - 1 - set) & 1);  // this set's last tile
+            if (j0 < tile0 + ntile && !(ok = wait(&ctl->o_done[set], (lastx >> 1) & 1, wc, 62))) break;
+            ctl->stat[set][q4 * 32 + lane] = make_float2(m_used, lrun);
+            if (!(ok = soft_sync())) break;  // both sets' sums and O
             tc_fence_after();
+            float M = -INFINITY, sum = 0.f, f[2];
+#pragma unroll
+            for (int i = 0; i < 2 * kRep; ++i) M = fmaxf(M, ctl->stat[i & 1][(i >> 1) * kRows + row].x);
+            const float Mr = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int i = 0; i < 2 * kRep; ++i) {
+                const float2 x = ctl->stat[i & 1][(i >> 1) * kRows + row];
+                const float fx = x.y == 0.f ? 0.f : fast_exp2(x.x - Mr);
+                sum += x.y == 0.f ? 0.f : x.y * fx;
+                if (i >> 1 == copy) f[i & 1] = fx;
+            }
             const bool whole = g.ntile == g.tiles;
-            const bool odd = ctl->nf_seg[seg & 7] == seg;
-            const float inv = whole ? (lrun == 0.f ? 0.f : 1.f / lrun) : 1.f;
-            float *part = a.workspace + ((size_t)blockIdx.x * 2 + (g.tile0 > 0 ? 0 : 1)) * kBM * (D + 2);
-            const size_t orow = ((size_t)g.b * a.T + tok) * a.Hq + g.h * sh.G + head;
+            const bool odd = ctl->nf_seg[(runs.n - 1) & 7] == runs.n - 1;
+            const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            float *part = a.workspace + ((size_t)blockIdx.x * 2 + (tile0 > 0 ? 0 : 1)) * kBM * (D + 2);
+            const size_t obase = (size_t)b * a.T;
+            if (valid && set == 0 && copy == 0) {
+                if (!whole) {
+                    part[row] = M;
+                    part[kBM + row] = sum;
+                } else if (a.lse) {
+                    const int hq = g.h * sh.G + (row0 + row) % sh.G;
+                    a.lse[((size_t)b * a.Hq + hq) * a.T + tok] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+                }
+            }
+            // This warp joins half of the dims (by its set) of its lanes' O; a set without a tile
+            // has f = 0 and whatever O the previous run left.
+            constexpr int kO = D / 2;
+            float *sX = reinterpret_cast<float *>(sQ);  // exchange of repeated rows: every QK of the run is done
 #pragma unroll 1
             for (int cc = 0; cc < kO / 32; ++cc) {
-                uint32_t r[32];
+                const int d0 = set * kO + cc * 32;
+                uint32_t ra[32], rb[32];
                 __syncwarp();
-                tmem_ld_32x32b_x32(tO + cc * 32, r);
-                tmem_ld_wait(r);
-                const int d0 = hc * kO + cc * 32;
-                if (odd && valid) {
-                    // Non-finite values of the nodes this row sees in this run of tiles.
-                    const int64_t lo = max(g.L, (int64_t)g.tile0 * kBN), hi = min(end, (int64_t)(g.tile0 + g.ntile) * kBN);
-                    for (int64_t slot = lo; slot < hi; ++slot) {
-                        if (!node_sees(a, g, tok, (int)(slot - g.L))) continue;
-                        const int page = page_of(a.pk, g.b, slot, a.status);
-                        if (page < 0) continue;
-                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.vpages) +
-                                                 (((size_t)page * a.pk.page_size + slot % a.pk.page_size) * sh.Hkv + g.h) * D + d0;
+                tmem_ld_32x32b_x32(tmem + F::TmemO + lane_off + d0, ra);
+                tmem_ld_32x32b_x32(tmem + F::TmemO + D + lane_off + d0, rb);
+                tmem_ld_wait(ra);
+                tmem_ld_wait(rb);
+                float o[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float x = __bfloat162float(v[i]);
-                            if (!isfinite(x)) r[i] = __float_as_uint(__uint_as_float(r[i]) + x);
+                for (int i = 0; i < 32; ++i)
+                    o[i] = (f[0] == 0.f ? 0.f : __uint_as_float(ra[i]) * f[0]) + (f[1] == 0.f ? 0.f : __uint_as_float(rb[i]) * f[1]);
+                if (odd && valid && copy == 0) {
+                    float t[32];  // (in local memory, only here)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) t[i] = o[i];
+                    add_nonfinite<32>(a, g, D, tok, d0, t);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = t[i];
+                }
+                if (kRep > 1) {
+                    // Rows of float4 units, the unit index swizzled by the row against bank conflicts.
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int unit = (d0 / 4 + i) ^ (lane & 7);
+                        *reinterpret_cast<float4 *>(sX + (q4 * 32 + lane) * D + unit * 4) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                } else if (valid) {
+                    if (!whole) {
+                        float4 *dst = reinterpret_cast<float4 *>(part + 2 * kBM + (size_t)row * D + d0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
+                        const size_t orow = (obase + tok) * a.Hq + g.h * sh.G + (row0 + row) % sh.G;
+                        if (a.out_f32) {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D + d0);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + d0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                                    pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                         }
                     }
                 }
-                if (!valid) continue;
-                if (!whole) {
-                    float4 *dst = reinterpret_cast<float4 *>(part + 2 * kBM + (size_t)row * D + d0);
+            }
+            if (kRep > 1) {
+                if (!(ok = soft_sync())) break;
+                // Copies summed, a float4 unit at a time, neighbouring threads on neighbouring units.
+                for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
+                    const int r = e / (D / 4), u = e % (D / 4);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float rs = 0.f, rm = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
-                                             __uint_as_float(r[4 * i + 3]));
-                } else if (a.out_f32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D + d0);
+                    for (int cp = 0; cp < kRep; ++cp) {
+                        const float4 x = *reinterpret_cast<const float4 *>(sX + (cp * kRows + r) * D + (u ^ (r & 7)) * 4);
+                        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
-                                             __uint_as_float(r[4 * i + 2]) * inv, __uint_as_float(r[4 * i + 3]) * inv);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + d0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv, __uint_as_float(r[8 * i + 2 * e + 1]) * inv);
-                        dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        for (int i = 0; i < 2; ++i) rm = fmaxf(rm, ctl->stat[i][cp * kRows + r].x);
                     }
+                    if (!whole) {
+                        *reinterpret_cast<float4 *>(part + 2 * kBM + (size_t)r * D + 4 * u) = o;
+                        continue;
+                    }
+#pragma unroll
+                    for (int cp = 0; cp < kRep; ++cp)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = ctl->stat[i][cp * kRows + r];
+                            rs += x.y == 0.f ? 0.f : x.y * fast_exp2(x.x - rm);
+                        }
+                    const float iv = rs == 0.f ? 0.f : 1.f / rs;
+                    const size_t off = ((obase + (row0 + r) / sh.G) * a.Hq + g.h * sh.G + (row0 + r) % sh.G) * D + 4 * u;
+                    if (a.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + off) = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + off) =
+                            make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
                 }
             }
-            if (valid && hc == 0) {
-                if (!whole) {
-                    part[row] = m_used;
-                    part[kBM + row] = lrun;
-                } else if (a.lse) {
-                    a.lse[((size_t)g.b * a.Hq + g.h * sh.G + head) * a.T + tok] =
-                        lrun == 0.f ? -INFINITY : (m_used + log2f(lrun)) * 0.69314718055994531f;
-                }
-            }
+            // The next run's queries and sums go where this one's were; O is overwritten by its
+            // first PV, which waits for these warps' P.
+            tc_fence_before();
+            runs.done(lane);
+            if (!(ok = soft_sync())) break;
         }
     }
 
@@ -961,7 +1158,7 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int rank, const cuuint6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool kPacked>
+template <int D, bool kPacked, int NC>
 cudaError_t launch(const TreeArgs &a, const WindowParams &wp, const RopeTurns &rt, cudaStream_t s) {
     const Shape sh = shape_of(a.B, a.T, a.Hq, a.Hkv);
     // One box covers a tile where pages hold whole tiles, half a tile otherwise.
@@ -980,14 +1177,14 @@ cudaError_t launch(const TreeArgs &a, const WindowParams &wp, const RopeTurns &r
         e = make_map(&tk, a.kpages, 4, dv, sv, bv, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (e != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(tree_decode_kernel<D, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Request)) !=
+    if ((e = cudaFuncSetAttribute(tree_decode_kernel<D, kPacked, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Request)) !=
         cudaSuccess)
         return e;
     // The in-kernel register split assumes this launch count: refuse to run otherwise.
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, tree_decode_kernel<D, kPacked>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, tree_decode_kernel<D, kPacked, NC>)) != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    tree_decode_kernel<D, kPacked><<<sh.groups * sh.R, kThreads, Cfg<D>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
+    tree_decode_kernel<D, kPacked, NC><<<sh.groups * sh.R, kThreads, Cfg<D>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.T * a.Hq;
     return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, sh);
@@ -1002,8 +1199,14 @@ size_t tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
 }
 
 cudaError_t launch_tree_decode(const TreeArgs &a, const WindowParams &wp, const RopeTurns &rt, cudaStream_t s) {
-    if (a.D == 128) return a.packed ? tree::launch<128, true>(a, wp, rt, s) : tree::launch<128, false>(a, wp, rt, s);
-    return a.packed ? tree::launch<64, true>(a, wp, rt, s) : tree::launch<64, false>(a, wp, rt, s);
+    // Columns per softmax warp: as many copies of the rows as the 128 MMA rows hold.
+    const int64_t rows = (int64_t)a.T * (a.Hq / a.Hkv);
+#define ATF_TREE(DD, PK)                                                 \
+    (rows <= 32 ? tree::launch<DD, PK, 32>(a, wp, rt, s)                 \
+                : rows <= 64 ? tree::launch<DD, PK, 64>(a, wp, rt, s) : tree::launch<DD, PK, 128>(a, wp, rt, s))
+    if (a.D == 128) return a.packed ? ATF_TREE(128, true) : ATF_TREE(128, false);
+    return a.packed ? ATF_TREE(64, true) : ATF_TREE(64, false);
+#undef ATF_TREE
 }
 
 }  // namespace atf
