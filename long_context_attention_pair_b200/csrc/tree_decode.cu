@@ -20,19 +20,20 @@
 // otherwise it leaves (max, sum, unscaled output) in the workspace, at most twice
 // per CTA (its first and its last item), and tree_merge_kernel joins them.
 //
-// Softmax.  Two sets of four warps take alternate key tiles, each with a running
-// max, sum and O accumulator of its own (joined at the end of a run of tiles), so
-// a set has two tile times for the chain S -> P -> PV and no row is shared between
-// warps.  NC is the number of a tile's columns that one warp takes: with at most 32
-// (64) rows the queries are repeated in all four (both halves) of the MMA's 128
-// rows and each copy takes a quarter (half) of the columns, P being zero in the
-// others, which shortens the chain where few rows leave the lanes empty.
+// Softmax.  Two sets of four warps take alternate key tiles; a row's two warps hand
+// its running max on from tile to tile and add into one O, so a set has two tile
+// times for its part of the chain S -> P -> PV.  NC is the number of a tile's columns
+// that one warp takes: with at most 32 (64) rows the queries are repeated in all four
+// (both halves) of the MMA's 128 rows and each copy takes a quarter (half) of the
+// columns, P being zero in the others, which shortens the chain where few rows leave
+// the lanes empty.  The copies' states are joined at the end of a run of tiles.
 //
 // Windows.  Inside one tile the distances span [d_min, d_max]: pairs r < r_lo are
 // pruned for every cell and their packed chunks not loaded, pairs r >= r_full are
-// kept for every cell and go through the MMA, and the boundary pairs between are
-// added per cell where the cell keeps them (the MMA sees zeros in their place, so
-// a pruned element takes no part whatever it holds).
+// kept for every cell.  Of a boundary pair in between, the keys that every row keeps
+// stay in the MMA's operand, the others are zeroed there, and those that some rows
+// keep (as many as the nodes' positions differ by; none for a single token) are added
+// per cell.  A pruned element thus takes no part whatever it holds.
 //
 // Precision.  q~ is kept as two bf16 parts (hi + lo, 2^-16 of its value), so
 // scores carry fp32-grade error; P is rounded to bf16 (the MMA's operand type,
@@ -58,10 +59,10 @@ constexpr int kBM = 128, kBN = 128;
 constexpr int kSoft = 8;
 constexpr int kProducer = 8, kQk = 9, kFix = 10, kPv = 11, kVProducer = 12, kSched = 13, kTail = 14;
 constexpr int kThreads = 32 * 16;
-// Registers: 128 per thread at launch; the last two warpgroups drop to 80 and the
-// two softmax warpgroups rise to 176, within the launch's total (checked here and,
+// Registers: 128 per thread at launch; the last two warpgroups drop to 72 and the
+// two softmax warpgroups rise to 184, within the launch's total (checked here and,
 // against the compiled kernel, at launch).
-constexpr int kLaunchRegs = 128, kSoftRegs = 176, kOtherRegs = 80;
+constexpr int kLaunchRegs = 128, kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
@@ -83,14 +84,11 @@ struct Cfg {
     static constexpr int OffKpos = OffStage + ST * StageBytes;   // [ST][128] key positions
     static constexpr int OffMask = OffKpos + ST * kBN * 4;       // [2][128] rows of 128 mask bits, one per node
     static constexpr int OffCtl = OffMask + 2 * kBM * 16;
-    static constexpr int CtlBytes = 4096;
+    static constexpr int CtlBytes = 6144;
     static constexpr int Request = OffCtl + CtlBytes + 1024;
     static_assert(Request <= 232448, "shared memory of one CTA");
-    // TMEM: S of set t at 128 t, O at 256 + D t.  P (64 columns of bf16 pairs): beside them for
-    // D = 64; for D = 128 over S, which its warps have read by then.
-    static constexpr bool PoverS = D == 128;
-    static constexpr uint32_t TmemO = 256, TmemCols = 512;
-    static constexpr uint32_t TmemP = PoverS ? 0 : 384, TmemPStep = PoverS ? 128 : 64;
+    // TMEM: S of set t at 128 t, P (64 columns of bf16 pairs) at 256 + 64 t, O at 384.
+    static constexpr uint32_t TmemP = 256, TmemO = 384, TmemCols = 512;
 };
 
 // One run of key tiles of one item.
@@ -109,16 +107,20 @@ struct Ctl {
     uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
     uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
     uint64_t m_full[2], m_empty[2];
+    uint64_t max_bar[2][4];          // per set and lane quarter: the running max after its tile is posted
     uint64_t drain, soft_bar;
     uint32_t tmem_base;
     int abort_flag;
     Segment seg[kRing];
-    int band[4][2];                  // (r_lo, r_full) of the tile in each stage
+    int4 band[4];                    // of the tile in each stage: (r_lo, rs, r_full, flags), see Band
+    uint32_t zone[4][kStaged];       // of staged pair rs + i: first key and end of the keys added per cell
     int nf_seg[8];                   // run (mod 8) whose tree holds a non-finite value
     int w[64];
+    uint64_t turn[64];
     float2 stat[2][kBM];             // (max, sum) of each set and MMA row
+    float run_max[2][kBM];           // running max after each set's latest tile
 };
-static_assert(sizeof(Ctl) <= 4096, "control block outgrew its space");
+static_assert(sizeof(Ctl) <= 6144, "control block outgrew its space");
 
 // What the scheduler needs to know of a sequence.
 struct Seq {
@@ -155,7 +157,10 @@ __device__ __forceinline__ int64_t units_before(const TreeArgs &a, const Shape &
 }
 // CTA groups with work, and the first unit of group g.
 __device__ __forceinline__ int active_groups(int64_t total, int groups) { return total < groups ? (int)total : groups; }
-__device__ __forceinline__ int64_t first_unit(int64_t total, int active, int g) { return (int64_t)g * total / active; }
+__device__ __forceinline__ int64_t first_unit(int64_t total, int active, int g) {
+    const int64_t x = (int64_t)g * total;
+    return x >> 31 ? x / active : (uint32_t)x / (uint32_t)active;  // the 64-bit division is a long subroutine
+}
 
 // Offset of 32-bit word `word` of row `row` in a K-step of 128 rows x 32 bytes
 // (SWIZZLE_32B), and of element d in 128-byte rows of 64 dims (SWIZZLE_128B, one
@@ -189,11 +194,17 @@ __device__ __forceinline__ void store_pair(uint8_t *tile, int row, int r, uint32
 // Pairs of one MMA K-step (packed) or of a K-step and its partner (natural).
 template <bool kPacked>
 constexpr int kPairsPerStep = kPacked ? 8 : 16;
-// Whether the fix-up warp touches a tile: boundary pairs to stage, or pairs that
-// its first K-step must not see.
+// How a tile's pairs are treated: r < r_lo pruned for every cell; [r_lo, rs) added per
+// cell for every key, straight from the K tile (only when more pairs are boundary
+// than can be staged); [rs, r_full) staged, the MMA keeping the keys that every row
+// keeps; r >= r_full kept for every cell.  The MMA starts at the K-step of rs.
+enum : int { kBandFix = 1, kBandCells = 2 };  // the fix-up warp has work; some cells are added
 template <bool kPacked>
-__device__ __forceinline__ bool needs_fix(int r_lo, int r_full) {
-    return r_lo < r_full || r_full % kPairsPerStep<kPacked> != 0;
+__device__ __forceinline__ int4 make_band(int r_lo, int r_full, bool spread) {
+    constexpr int kPer = kPairsPerStep<kPacked>;
+    const int rs = r_full - r_lo > kStaged ? (r_full - kStaged + kPer - 1) / kPer * kPer : r_lo;
+    const int flags = (r_lo < r_full || rs % kPer != 0 ? kBandFix : 0) | (r_lo < rs || (spread && r_lo < r_full) ? kBandCells : 0);
+    return make_int4(r_lo, rs, r_full, flags);
 }
 
 __device__ __forceinline__ int first_kept(const int *w, int H, int64_t d) {
@@ -285,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     using F = Cfg<D>;
     constexpr int H = F::H, C = F::C, ST = F::ST;
     constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
-    constexpr int CW = NC < 64 ? NC : 64;               // columns in registers at a time
     constexpr int kPer = kPairsPerStep<kPacked>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -321,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&ctl->o_done[s], 1);
                 mbar_init(&ctl->m_full[s], 2);
                 mbar_init(&ctl->m_empty[s], 4);
+                for (int q = 0; q < 4; ++q) mbar_init(&ctl->max_bar[s][q], 1);
             }
             mbar_init(&ctl->drain, 2);
             mbar_init(&ctl->soft_bar, kSoft);
@@ -334,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) prefetch_tmap(&tm_v);
     } else if (warp == kFix) {
         for (int r = lane; r < H; r += 32) ctl->w[r] = wp.w[r];
+    } else if (warp == kTail) {
+        // (Read by lane from shared memory later: a parameter indexed by lane costs a pass per lane.)
+        for (int r = lane; r < H; r += 32) ctl->turn[r] = rt.turn[r];
     }
     tc_fence_before();
     __syncthreads();
@@ -351,30 +365,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ scheduler
         // This group's run of units: the total, then the sequence that holds the first.
         const int member = blockIdx.x % sh.R, group = blockIdx.x / sh.R;
-        const int64_t total = units_before(a, sh, sh.B);
+        Seq ls{};  // this lane's sequence of the first 32
+        int64_t ln = 0, total = 0;
+        for (int b0 = 0; b0 < sh.B; b0 += 32) {
+            const Seq x = b0 + lane < sh.B ? seq_of(a, sh, b0 + lane) : Seq{};
+            const int64_t n = units_of(x, sh.Hkv);
+            if (b0 == 0) ls = x, ln = n;
+            total += n;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         const int active = active_groups(total, sh.groups);
         const int64_t u0 = group < active ? first_unit(total, active, group) : 0;
         int64_t left = (group < active ? first_unit(total, active, group + 1) : 0) - u0, off = 0, base = 0;
         int b = 0;
+        Seq s{};
         for (int b0 = 0; b0 < sh.B && left > 0; b0 += 32) {
-            const int64_t n = b0 + lane < sh.B ? units_of(seq_of(a, sh, b0 + lane), sh.Hkv) : 0;
-            int64_t incl = n;
+            if (b0 > 0) {
+                ls = b0 + lane < sh.B ? seq_of(a, sh, b0 + lane) : Seq{};
+                ln = units_of(ls, sh.Hkv);
+            }
+            int64_t incl = ln;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            const uint32_t m = __ballot_sync(0xffffffffu, u0 >= base + incl - n && u0 < base + incl);
+            const uint32_t m = __ballot_sync(0xffffffffu, u0 >= base + incl - ln && u0 < base + incl);
             if (m) {
                 const int src = __ffs(m) - 1;
                 b = b0 + src;
-                off = u0 - __shfl_sync(0xffffffffu, base + incl - n, src);
+                off = u0 - __shfl_sync(0xffffffffu, base + incl - ln, src);
+                s.L = __shfl_sync(0xffffffffu, ls.L, src);
+                s.nodes = __shfl_sync(0xffffffffu, ls.nodes, src);
+                s.tiles = __shfl_sync(0xffffffffu, ls.tiles, src);
+                s.groups = __shfl_sync(0xffffffffu, ls.groups, src);
                 break;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
-        Seq s{};
-        if (left > 0) s = seq_of(a, sh, b);
         for (int n = 0; ok; ++n) {
             Segment g{};
             while (left > 0) {
@@ -383,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s = seq_of(a, sh, ++b);
                     continue;
                 }
-                const int item = (int)(off / s.tiles);
+                const int item = (int)(off >> 31 ? off / s.tiles : (uint32_t)off / (uint32_t)s.tiles);
                 g.b = b;
                 g.h = item / s.groups;
                 g.L = (int)s.L;
@@ -464,10 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 const int ca = v || !kPacked ? 0 : r_lo >> 3;
                 if (lane == 0) {
-                    if (!v) {
-                        ctl->band[st][0] = r_lo;
-                        ctl->band[st][1] = r_full;
-                    }
+                    if (!v) ctl->band[st] = make_band<kPacked>(r_lo, r_full, g.pmin != g.pmax);
                     mbar_expect_tx(&full[st], (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves);
                 }
                 __syncwarp();
@@ -495,28 +521,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = it % ST;
                 const int64_t m0 = (int64_t)j * kBN;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
-                const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
-                if (!needs_fix<kPacked>(r_lo, r_full)) continue;
+                const int4 bd = ctl->band[st];
+                if (!(bd.w & kBandFix)) continue;
                 uint8_t *kst = sK + st * F::TileBytes;
-                if (r_lo < r_full) {
-                    int *kp = sKpos + st * kBN;
-                    for (int e = lane; e < kBN; e += 32) {
-                        const int64_t slot = m0 + e;
-                        kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
+                constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
+                int kp[kK];
+#pragma unroll
+                for (int e = 0; e < kK; ++e) {
+                    const int64_t slot = m0 + lane + 32 * e;
+                    kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
+                    if (bd.w & kBandCells) sKpos[st * kBN + lane + 32 * e] = kp[e];
+                }
+                // Pairs below rs that share its K-step are pruned for every cell.
+                for (int r = bd.y / kPer * kPer; r < bd.y; ++r)
+#pragma unroll
+                    for (int e = 0; e < kK; ++e) store_pair<D, kPacked>(kst, lane + 32 * e, r, 0u);
+                for (int r = bd.y; r < bd.z; ++r) {
+                    // Keys at positions >= all are kept by every row, below none by no row.
+                    const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
+                    int z0 = kBN, z1 = 0;
+#pragma unroll
+                    for (int e = 0; e < kK; ++e) {
+                        const bool some = kp[e] < all && kp[e] >= none;
+                        if (kp[e] < all) {
+                            if (some) sStage[(st * kStaged + r - bd.y) * kBN + lane + 32 * e] = load_pair<D, kPacked>(kst, lane + 32 * e, r);
+                            store_pair<D, kPacked>(kst, lane + 32 * e, r, 0u);
+                        }
+                        const uint32_t m = __ballot_sync(0xffffffffu, some);
+                        if (m) z0 = min(z0, 32 * e + __ffs(m) - 1), z1 = 32 * e + 32 - __clz(m);
                     }
-                    const int rs = max(r_lo, r_full - kStaged), nb = r_full - rs;
-                    uint32_t *sw = sStage + st * (kStaged * kBN);
-                    for (int e = lane; e < nb * kBN; e += 32)
-                        sw[e] = load_pair<D, kPacked>(kst, e & (kBN - 1), rs + (e >> 7));
-                    __syncwarp();
+                    if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
                 }
-                // Pairs of the first K-step of the MMA that are not kept by every cell.
-                const int z0 = r_full / kPer * kPer;
-                if (r_full > z0) {
-                    const int nz = r_full - z0;
-                    for (int e = lane; e < nz * kBN; e += 32) store_pair<D, kPacked>(kst, e & (kBN - 1), z0 + (e >> 7), 0u);
-                    fence_proxy_async_smem();
-                }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
             }
@@ -598,18 +634,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; ok && j < ntile; ++j, ++it) {
                 const int st = it % ST, set = it & 1;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
-                const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
-                if (needs_fix<kPacked>(r_lo, r_full)) {
+                const int4 bd = ctl->band[st];
+                if (bd.w & kBandFix) {
                     if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
                     fixed ^= 1u << st;
                 }
-                // S of this set is free once it has been read, or, with P over it, once P has.
-                if (it >= 2 && !(ok = wait(F::PoverS ? &ctl->o_done[set] : &ctl->s_read[set], ((it >> 1) - 1) & 1, wc, 49))) break;
+                if (it >= 2 && !(ok = wait(&ctl->s_read[set], ((it >> 1) - 1) & 1, wc, 49))) break;
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + set * kBN;
                     uint32_t acc = 0;
-                    for (int c = r_full / kPer; c < H / kPer; ++c) {
+                    for (int c = bd.y / kPer; c < H / kPer; ++c) {
 #pragma unroll
                         for (int part = 0; part < (kPacked ? 1 : 2); ++part) {
                             // Packed: one K-step is 8 whole pairs.  Natural: 16 dims of the low half,
@@ -653,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk) {
                         const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
-                        umma_bf16_ts(tmem + F::TmemO + set * D, tmem + F::TmemP + set * F::TmemPStep + kk * 8, db, idesc,
-                                     (j >= tile0 + 2 || kk > 0) ? 1u : 0u);
+                        umma_bf16_ts(tmem + F::TmemO, tmem + F::TmemP + set * 64 + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
                     }
                     umma_commit(&ctl->o_done[set]);
                     umma_commit(&ctl->v_empty[st]);
@@ -671,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (q4 * 32) % kRows + lane;        // row of the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const uint32_t tS = tmem + set * kBN + lane_off;
-        const uint32_t tP = tmem + F::TmemP + set * F::TmemPStep + lane_off;
-        const uint32_t tO = tmem + F::TmemO + set * D + lane_off;
+        const uint32_t tP = tmem + F::TmemP + set * 64 + lane_off;
+        const uint32_t tO = tmem + F::TmemO + lane_off;
         const float scale_log2 = 1.4426950408889634f * rsqrtf((float)D);
         uint32_t fixed = 0;                              // phase bit of k_ready per stage
         int syncs = 0, tails = 0;
@@ -682,11 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&ctl->soft_bar);
             return wait(&ctl->soft_bar, syncs++ & 1, wc, 53);
         };
-        uint32_t zero[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) zero[i] = 0;
-        if (!F::PoverS && kRep > 1) {
+        if (kRep > 1) {
             // P is zero in the other copies' columns for good.
+            uint32_t zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
 #pragma unroll
             for (int i = 0; i < kRep; ++i)
                 if (i != copy)
@@ -729,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (rr >= rows) break;
                         if (ts[u] != last) {
                             last = ts[u];
-                            cs = turn_cos_sin(node_pos(a, b, L, last), rt.turn[pr]);
+                            cs = turn_cos_sin(node_pos(a, b, L, last), ctl->turn[pr]);
                         }
                         const float fa = __bfloat162float(xa[u]), fb = __bfloat162float(xb[u]);
                         const float x = fa * cs.x - fb * cs.y, y = fb * cs.x + fa * cs.y;
@@ -749,139 +783,161 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = valid ? node_pos(a, b, L, tok) : 0;
             if (!(ok = wait(&ctl->q_ready, (runs.n - 1) & 1, wc, 54))) break;  // the other warps' pairs, for the boundary
 
-            float m_used = -INFINITY, lrun = 0.f;
+            float m_used = -INFINITY, lrun = 0.f;  // this set's sum, scaled by its latest running max
+            const int pmax = g.pmax;
             const int j0 = tile0 + ((it ^ set) & 1);  // this set's tiles
             for (int j = j0; j < tile0 + ntile; j += 2) {
                 const int x = it + (j - tile0), st = x % ST;
-                if (!(ok = wait(&ctl->k_full[st], (x / ST) & 1, wc, 55))) break;
-                const int r_lo = ctl->band[st][0], r_full = ctl->band[st][1];
-                const bool fix = needs_fix<kPacked>(r_lo, r_full), boundary = r_lo < r_full;
                 const bool tail = (int64_t)(j + 1) * kBN > L;
+                if (!(ok = wait(&ctl->k_full[st], (x / ST) & 1, wc, 55))) break;
+                const int4 bd = ctl->band[st];
+                const bool cells = bd.w & kBandCells;
                 __syncwarp();
-                if (!boundary && lane == 0) mbar_arrive(&ctl->k_empty[st]);  // nothing else of K is read here
+                if (!cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);  // nothing of the stage is read here
                 if (!(ok = wait(&ctl->s_full[set], (x >> 1) & 1, wc, 56))) break;
                 tc_fence_after();
-                if (fix) {
-                    // Waited for only where this warp still holds the stage (boundary pairs), so that
-                    // the barrier cannot be a phase ahead of it.
-                    if (boundary && !(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 57))) break;
+                bool dense = bd.y < H;  // S holds something
+                if (bd.w & kBandFix) {
+                    // Waited for only where this warp still holds the stage, so that the barrier
+                    // cannot be a phase ahead of it.
+                    if (cells && !(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 57))) break;
                     fixed ^= 1u << st;
                 }
                 if (tail) {
                     if (!(ok = wait(&ctl->m_full[set], tails & 1, wc, 58))) break;
                     ++tails;
                 }
-                // The row's maximum, CW columns at a time, the first ones last: they stay in
-                // registers for the exponentials (128 columns at once would spill); the others are
-                // read again, after having been written back where the tensor core's scores were
-                // not the last word.
-                float s[CW], mx = -INFINITY;
+                if (cells || tail) {
+                    // Cells added or hidden, in S itself, 32 columns at a time.
 #pragma unroll 1
-                for (int part = NC / CW - 1; part >= 0 && live; --part) {
-                    const int cc = c0 + part * CW;
-                    if (r_full < H) {
-                        uint32_t ra[CW];
-                        if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + cc, ra);
-                        else tmem_ld_32x32b_x32(tS + cc, ra);
-                        tmem_ld_wait(ra);
+                    for (int cc = c0; live && cc < c0 + NC; cc += 32) {
+                        uint32_t ra[32];
+                        float s[32];
+                        __syncwarp();
+                        if (dense) {
+                            tmem_ld_32x32b_x32(tS + cc, ra);
+                            tmem_ld_wait(ra);
 #pragma unroll
-                        for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
-                    } else {
+                            for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(ra[i]);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < CW; ++i) s[i] = 0.f;
-                    }
-                    if (boundary) {
-                        const uint8_t *kst = sK + st * F::TileBytes;
-                        const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + cc);
-                        const int rs = max(r_lo, r_full - kStaged);
+                            for (int i = 0; i < 32; ++i) s[i] = 0.f;
+                        }
+                        if (cells) {
+                            const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + cc);
 #pragma unroll 1
-                        for (int r = r_lo; r < r_full; ++r) {
-                            // Keys at positions >= lim keep the pair.
-                            const int64_t l64 = (int64_t)pos - w[r];
-                            const int lim = !valid ? INT32_MAX : (l64 < INT32_MIN ? INT32_MIN : (int)l64);
-                            const uint32_t qh = load_pair<D, kPacked>(sQ, copy * kRows + row, r);
-                            const uint32_t ql = load_pair<D, kPacked>(sQ + F::TileBytes, copy * kRows + row, r);
-                            const float qa = bf16lo(qh) + bf16lo(ql), qb = bf16hi(qh) + bf16hi(ql);
-                            auto add4 = [&](int i, uint4 k) {
-                                const int4 p = kp[i];
-                                s[4 * i] += p.x >= lim ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
-                                s[4 * i + 1] += p.y >= lim ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
-                                s[4 * i + 2] += p.z >= lim ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
-                                s[4 * i + 3] += p.w >= lim ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
-                            };
-                            if (r >= rs) {
-                                const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + st * (kStaged * kBN) + (r - rs) * kBN + cc);
+                            for (int r = bd.x; r < bd.z; ++r) {
+                                if (r >= bd.y) {
+                                    const uint32_t z = ctl->zone[st][r - bd.y];
+                                    if ((int)(z >> 16) <= cc || (int)(z & 0xffff) >= cc + 32) continue;
+                                }
+                                const uint32_t qh = load_pair<D, kPacked>(sQ, copy * kRows + row, r);
+                                const uint32_t ql = load_pair<D, kPacked>(sQ + F::TileBytes, copy * kRows + row, r);
+                                const float qa = bf16lo(qh) + bf16lo(ql), qb = bf16hi(qh) + bf16hi(ql);
+                                // This row keeps keys at positions >= lim; of a staged pair the MMA has
+                                // those at lim + span and beyond (differences modulo 2^32 are exact here).
+                                const int lim = pos - w[r];
+                                if (r >= bd.y) {
+                                    const uint32_t span = (uint32_t)(pmax - pos);
+                                    const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + (st * kStaged + r - bd.y) * kBN + cc);
 #pragma unroll
-                                for (int i = 0; i < CW / 4; ++i) add4(i, kw[i]);
-                            } else {
-                                // More boundary pairs than staged: those below are whole in the K tile.
+                                    for (int i = 0; i < 8; ++i) {
+                                        const uint4 k = kw[i];
+                                        const int4 p = kp[i];
+                                        s[4 * i] += (uint32_t)(p.x - lim) < span ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
+                                        s[4 * i + 1] += (uint32_t)(p.y - lim) < span ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
+                                        s[4 * i + 2] += (uint32_t)(p.z - lim) < span ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
+                                        s[4 * i + 3] += (uint32_t)(p.w - lim) < span ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
+                                    }
+                                } else {
+                                    const uint8_t *kst = sK + st * F::TileBytes;
 #pragma unroll
-                                for (int i = 0; i < CW / 4; ++i) {
-                                    uint4 k;
-                                    k.x = load_pair<D, kPacked>(kst, cc + 4 * i, r);
-                                    k.y = load_pair<D, kPacked>(kst, cc + 4 * i + 1, r);
-                                    k.z = load_pair<D, kPacked>(kst, cc + 4 * i + 2, r);
-                                    k.w = load_pair<D, kPacked>(kst, cc + 4 * i + 3, r);
-                                    add4(i, k);
+                                    for (int i = 0; i < 32; ++i) {
+                                        const uint32_t k = load_pair<D, kPacked>(kst, cc + i, r);
+                                        s[i] += sKpos[st * kBN + cc + i] >= lim ? fmaf(qa, bf16lo(k), qb * bf16hi(k)) : 0.f;
+                                    }
                                 }
                             }
                         }
-                    }
-                    if (tail) {
-                        const uint32_t *mask = reinterpret_cast<const uint32_t *>(sMask + set * kBM + (tok - row0 / sh.G)) + cc / 32;
+                        if (tail) {
+                            const uint32_t see = reinterpret_cast<const uint32_t *>(sMask + set * kBM + (tok - row0 / sh.G))[cc / 32];
 #pragma unroll
-                        for (int i = 0; i < CW / 32; ++i) {
-                            const uint32_t see = mask[i];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1u)) s[i] = -INFINITY;
                         }
-                    }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < CW; i += 8) {
-                        mx = max3(mx, s[i], s[i + 1]);
-                        mx0 = max3(mx0, s[i + 2], s[i + 3]);
-                        mx1 = max3(mx1, s[i + 4], s[i + 5]);
-                        mx2 = max3(mx2, s[i + 6], s[i + 7]);
-                    }
-                    mx = fmaxf(fmaxf(mx, mx0), fmaxf(mx1, mx2));
-                    if (part > 0 && (boundary || tail || r_full >= H)) {
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < CW; i += 32) tmem_st_32x32b_x32(tS + cc + i, *reinterpret_cast<uint32_t(*)[32]>(&s[i]));
-                        tmem_st_wait();
+                        for (int i = 0; i < 32; ++i) ra[i] = __float_as_uint(s[i]);
+                        tmem_st_32x32b_x32(tS + cc, ra);
                     }
+                    tmem_st_wait();
+                    dense = true;
+                    __syncwarp();
+                    if (cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);
+                    if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
                 }
+                // The row's columns, in registers from here on.
+                float s[NC];
+                if (dense) {
+                    // (Loads of 128 columns do not compile for a kernel launched with 128 registers.)
+                    constexpr int kLd = NC == 32 ? 32 : 64;
+                    uint32_t ra[NC / kLd][kLd];
+#pragma unroll
+                    for (int i = 0; i < NC / kLd; ++i) {
+                        if constexpr (kLd == 64) tmem_ld_32x32b_x64(tS + c0 + 64 * i, ra[i]);
+                        else tmem_ld_32x32b_x32(tS + c0, ra[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NC / kLd; ++i) tmem_ld_wait(ra[i]);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) s[i] = __uint_as_float(ra[i / kLd][i % kLd]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) s[i] = 0.f;
+                }
+                tc_fence_before();
                 __syncwarp();
-                if (boundary && lane == 0) mbar_arrive(&ctl->k_empty[st]);
-                if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
-                // The running max is kept unless it grew by more than 2^8: O / l uses the same one,
-                // so the result does not depend on it.
-                const float tile_max = mx * scale_log2;
-                const bool need = live && tile_max > m_used + kRescaleThreshold;
-                const float m_new = need ? tile_max : m_used;
-                const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+                if (lane == 0) mbar_arrive(&ctl->s_read[set]);
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NC; i += 8) {
+                    mx0 = max3(mx0, s[i], s[i + 1]);
+                    mx1 = max3(mx1, s[i + 2], s[i + 3]);
+                    mx2 = max3(mx2, s[i + 4], s[i + 5]);
+                    mx3 = max3(mx3, s[i + 6], s[i + 7]);
+                }
+                const float tile_max = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale_log2;
+                // The running max after the previous tile, from the row's warp of the other set.  It is
+                // kept unless it grew by more than 2^8: O / l uses the same one, so the result does not
+                // depend on it.
+                float m_prev = -INFINITY;
+                if (j > tile0) {
+                    if (!(ok = wait(&ctl->max_bar[set ^ 1][q4], ((x - 1) >> 1) & 1, wc, 63))) break;
+                    m_prev = ctl->run_max[set ^ 1][q4 * 32 + lane];
+                }
+                const bool need = tile_max > m_prev + kRescaleThreshold;
+                const float m_new = need ? tile_max : m_prev;
+                ctl->run_max[set][q4 * 32 + lane] = m_new;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->max_bar[set][q4]);
+                if (m_new != m_used) lrun *= fast_exp2(m_used - m_new);
                 m_used = m_new;
-                const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen so far
+                const float mr = m_new == -INFINITY ? 0.f : m_new;  // nothing seen so far
                 const float2 mneg = make_float2(-mr, -mr), sc2 = make_float2(scale_log2, scale_log2);
                 float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int part = 0; part < NC / CW; ++part) {
-                    uint32_t pk[CW / 2];
-                    if (live) {
-                        if (part > 0) {
-                            uint32_t ra[CW];
-                            if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + c0 + part * CW, ra);
-                            else tmem_ld_32x32b_x32(tS + c0 + part * CW, ra);
-                            tmem_ld_wait(ra);
+                // P of this set is free once its previous PV is done.
+                if (x >= 2) {
+                    if (!(ok = wait(&ctl->o_done[set], ((x >> 1) - 1) & 1, wc, 61))) break;
+                    tc_fence_after();
+                }
+                if (live) {
 #pragma unroll
-                            for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
-                        }
+                    for (int q = 0; q < NC; q += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < CW / 2; i += 2) {
-                            float2 xa = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mneg);
-                            float2 xb = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), sc2, mneg);
+                        for (int i = 0; i < 16; i += 2) {
+                            float2 xa = fma2(make_float2(s[q + 2 * i], s[q + 2 * i + 1]), sc2, mneg);
+                            float2 xb = fma2(make_float2(s[q + 2 * i + 2], s[q + 2 * i + 3]), sc2, mneg);
                             xa.x = fast_exp2(xa.x);
                             xa.y = fast_exp2(xa.y);
                             xb.x = fast_exp2(xb.x);
@@ -891,74 +947,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pk[i] = pack_bf16x2(xa.x, xa.y);
                             pk[i + 1] = pack_bf16x2(xb.x, xb.y);
                         }
+                        tmem_st_x16(tP + (c0 + q) / 2, pk);
                     }
-                    if (part == NC / CW - 1 && !F::PoverS) {
-                        // S has been read.
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->s_read[set]);
-                    }
-                    // P and O of this set are free once its previous PV is done (with P over S, this
-                    // tile's QK has waited for that).  Every warp waits, also one without rows: its
-                    // arrivals must not run ahead of the others'.
-                    if (part == 0) {
-                        if (!F::PoverS && x >= 2) {
-                            if (!(ok = wait(&ctl->o_done[set], ((x >> 1) - 1) & 1, wc, 61))) break;
-                            tc_fence_after();
-                        }
-                        if (j >= tile0 + 2 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-                            for (int cc = 0; cc < D / 32; ++cc) {
-                                uint32_t r[32];
-                                tmem_ld_32x32b_x32(tO + cc * 32, r);
-                                tmem_ld_wait(r);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                                tmem_st_32x32b_x32(tO + cc * 32, r);
-                            }
-                        }
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int i = 0; i < CW / 32; ++i) tmem_st_x16(tP + (c0 + part * CW) / 2 + 16 * i, pk + 16 * i);
-                    }
-                }
-                if (!ok) break;
-                if (live) {
-                    if (F::PoverS && kRep > 1) {
-#pragma unroll
-                        for (int i = 0; i < kRep; ++i)
-                            if (i != copy) {
-#pragma unroll
-                                for (int y = 0; y < NC / 32; ++y) tmem_st_x16(tP + i * (NC / 2) + 16 * y, zero);
-                            }
-                    }
-                    tmem_st_wait();
                     const float2 ls = add2(l0, l1);
-                    lrun = lrun * alpha + (ls.x + ls.y);
+                    lrun += ls.x + ls.y;
                 }
+                if (j > tile0 && __any_sync(0xffffffffu, need)) {
+                    // O may be rescaled once the previous tile's PV is done.
+                    if (!(ok = wait(&ctl->o_done[set ^ 1], ((x - 1) >> 1) & 1, wc, 64))) break;
+                    tc_fence_after();
+                    const float alpha = need ? fast_exp2(m_prev - m_new) : 1.f;
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(tO + cc * 32, r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                        tmem_st_32x32b_x32(tO + cc * 32, r);
+                    }
+                }
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->p_full[set]);
             }
             if (!ok) break;
             it += ntile;
-            // ---- end of the run: the sets' (and copies') states of each row joined
+            // ---- end of the run: the sets' sums and the copies' states of each row joined
             const int lastx = it - 1 - ((it - 1 - set) & 1);  // this set's last tile
             if (j0 < tile0 + ntile && !(ok = wait(&ctl->o_done[set], (lastx >> 1) & 1, wc, 62))) break;
             ctl->stat[set][q4 * 32 + lane] = make_float2(m_used, lrun);
-            if (!(ok = soft_sync())) break;  // both sets' sums and O
+            if (!(ok = soft_sync())) break;  // both sets' sums, and O
             tc_fence_after();
-            float M = -INFINITY, sum = 0.f, f[2];
+            // O of a copy is scaled by the running max after the run's last tile; a set's sum by that
+            // after its own.
+            const int lset = (it - 1) & 1;
+            float M = -INFINITY, sum = 0.f, f = 1.f;
 #pragma unroll
-            for (int i = 0; i < 2 * kRep; ++i) M = fmaxf(M, ctl->stat[i & 1][(i >> 1) * kRows + row].x);
+            for (int cp = 0; cp < kRep; ++cp) M = fmaxf(M, ctl->stat[lset][cp * kRows + row].x);
             const float Mr = M == -INFINITY ? 0.f : M;
 #pragma unroll
-            for (int i = 0; i < 2 * kRep; ++i) {
-                const float2 x = ctl->stat[i & 1][(i >> 1) * kRows + row];
-                const float fx = x.y == 0.f ? 0.f : fast_exp2(x.x - Mr);
-                sum += x.y == 0.f ? 0.f : x.y * fx;
-                if (i >> 1 == copy) f[i & 1] = fx;
+            for (int cp = 0; cp < kRep; ++cp) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 y = ctl->stat[i][cp * kRows + row];
+                    sum += y.y == 0.f ? 0.f : y.y * fast_exp2(y.x - Mr);
+                }
+                if (cp == copy) f = fast_exp2(ctl->stat[lset][cp * kRows + row].x - Mr);
             }
             const bool whole = g.ntile == g.tiles;
             const bool odd = ctl->nf_seg[(runs.n - 1) & 7] == runs.n - 1;
@@ -974,23 +1010,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.lse[((size_t)b * a.Hq + hq) * a.T + tok] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
                 }
             }
-            // This warp joins half of the dims (by its set) of its lanes' O; a set without a tile
-            // has f = 0 and whatever O the previous run left.
+            // This warp takes half of the dims (by its set) of its lanes' O.
             constexpr int kO = D / 2;
             float *sX = reinterpret_cast<float *>(sQ);  // exchange of repeated rows: every QK of the run is done
 #pragma unroll 1
             for (int cc = 0; cc < kO / 32; ++cc) {
                 const int d0 = set * kO + cc * 32;
-                uint32_t ra[32], rb[32];
+                uint32_t ra[32];
                 __syncwarp();
-                tmem_ld_32x32b_x32(tmem + F::TmemO + lane_off + d0, ra);
-                tmem_ld_32x32b_x32(tmem + F::TmemO + D + lane_off + d0, rb);
+                tmem_ld_32x32b_x32(tO + d0, ra);
                 tmem_ld_wait(ra);
-                tmem_ld_wait(rb);
                 float o[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    o[i] = (f[0] == 0.f ? 0.f : __uint_as_float(ra[i]) * f[0]) + (f[1] == 0.f ? 0.f : __uint_as_float(rb[i]) * f[1]);
+                    o[i] = kRep > 1 ? __uint_as_float(ra[i]) * f : __uint_as_float(ra[i]);
                 if (odd && valid && copy == 0) {
                     float t[32];  // (in local memory, only here)
 #pragma unroll
@@ -1029,31 +1062,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (kRep > 1) {
+                if (set == 0 && copy == 0) ctl->run_max[0][row] = inv;  // for the threads that write the row
                 if (!(ok = soft_sync())) break;
                 // Copies summed, a float4 unit at a time, neighbouring threads on neighbouring units.
                 for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
                     const int r = e / (D / 4), u = e % (D / 4);
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float rs = 0.f, rm = -INFINITY;
 #pragma unroll
                     for (int cp = 0; cp < kRep; ++cp) {
                         const float4 x = *reinterpret_cast<const float4 *>(sX + (cp * kRows + r) * D + (u ^ (r & 7)) * 4);
                         o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) rm = fmaxf(rm, ctl->stat[i][cp * kRows + r].x);
                     }
                     if (!whole) {
                         *reinterpret_cast<float4 *>(part + 2 * kBM + (size_t)r * D + 4 * u) = o;
                         continue;
                     }
-#pragma unroll
-                    for (int cp = 0; cp < kRep; ++cp)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 x = ctl->stat[i][cp * kRows + r];
-                            rs += x.y == 0.f ? 0.f : x.y * fast_exp2(x.x - rm);
-                        }
-                    const float iv = rs == 0.f ? 0.f : 1.f / rs;
+                    const float iv = ctl->run_max[0][r];
                     const size_t off = ((obase + (row0 + r) / sh.G) * a.Hq + g.h * sh.G + (row0 + r) % sh.G) * D + 4 * u;
                     if (a.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + off) = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
                     else
