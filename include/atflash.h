@@ -421,7 +421,8 @@ int atflash_cache_append_theta(const void *k, const int64_t *k_strides, const vo
  * seqlens[b] + j, position positions[b][j]); pair r of a key enters the score
  * while positions[b][i] - (the key's position) <= w_r (a negative distance is
  * kept).  With T = 1 this is atflash_decode_paged for the token in the last slot.
- *   q          strided [B][T][Hq][D] bf16, un-rotated; rotated here by positions.
+ *   q          strided [B][T][Hq][D] bf16, un-rotated (strides multiples of 8
+ *              elements); rotated here by positions.
  *   tree_mask  device uint8 [B][T][T], entry (b, i, j) != 0: node i sees node j
  *              (also its own entry, and entries j > i); NULL: j <= i (a chain).
  *   positions  device int32 [B][T] >= 0, or NULL: seqlens[b] + i.

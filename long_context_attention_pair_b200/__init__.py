@@ -599,7 +599,7 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
                       workspace=None, stream=None, theta=None):
     """Windowed attention of a tree of drafted tokens over a paged cache with rotated keys.
 
-    q [B, T, Hq, D] bf16 (un-rotated; any strides with contiguous dims): node i of
+    q [B, T, Hq, D] bf16 (un-rotated; strides multiples of 8, dims contiguous): node i of
     sequence b sits at positions[b, i] (seqlens[b] + i by default), attends the
     seqlens[b] committed slots and the nodes j with tree_mask[b, i, j] ([B, T, T]
     uint8 or bool; j <= i by default), whose keys and values ``cache_append`` put in

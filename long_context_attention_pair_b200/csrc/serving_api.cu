@@ -184,7 +184,8 @@ int atflash_tree_decode_paged_theta(const void *q, const int64_t *q_strides, con
     if ((rc = check_table(B, max_pages, page_size)) != ATFLASH_OK) return rc;
     if (!theta_valid(D, theta) || isnan(k_window) || k_window < 0.0) return ATFLASH_ERR_INVALID_ARG;
     if (out_dtype != ATFLASH_F32 && out_dtype != ATFLASH_BF16) return ATFLASH_ERR_UNSUPPORTED;
-    if (!aligned(q, 16) || !aligned(kpages, 16) || !aligned(vpages, 16) || !aligned(out, 16))
+    const Strides qs = strides_of(q_strides, T, Hq, D);
+    if (!aligned(q, 16) || !aligned(kpages, 16) || !aligned(vpages, 16) || !aligned(out, 16) || !multiple_of(qs, 8))
         return ATFLASH_ERR_ALIGNMENT;
     const size_t need = tree_workspace_bytes(B, T, Hq, Hkv, D);
     if (!workspace || workspace_bytes < need) return ATFLASH_ERR_WORKSPACE;
@@ -198,7 +199,7 @@ int atflash_tree_decode_paged_theta(const void *q, const int64_t *q_strides, con
     wp.H = D / 2;
     for (int r = 0; r < D / 2; ++r) wp.w[r] = (int32_t)w[r], wp.theta[r] = theta[r];
     TreeArgs a{};
-    a.q = q, a.qs = strides_of(q_strides, T, Hq, D);
+    a.q = q, a.qs = qs;
     a.kpages = kpages, a.vpages = vpages;
     a.pk = PagedKV{block_table, max_pages, page_size, num_pages};
     a.seqlens = seqlens, a.positions = positions, a.counts = counts, a.mask = tree_mask;

@@ -113,6 +113,7 @@ struct Ctl {
     int abort_flag;
     Segment seg[kRing];
     int4 band[4];                    // of the tile in each stage: (r_lo, rs, r_full, flags), see Band
+    uint32_t chunks[4];              // 32-key chunks of the tile in which cells are added
     uint32_t zone[4][kStaged];       // of staged pair rs + i: first key and end of the keys added per cell
     int nf_seg[8];                   // run (mod 8) whose tree holds a non-finite value
     int w[64];
@@ -182,14 +183,22 @@ __device__ __forceinline__ uint32_t load_pair(const uint8_t *tile, int row, int 
         return lo | (uint32_t) * reinterpret_cast<const uint16_t *>(tile + sw128_off(row, r + D / 2)) << 16;
     }
 }
+// Pairs r .. r + 3 (r a multiple of 4) of a row.
 template <int D, bool kPacked>
-__device__ __forceinline__ void store_pair(uint8_t *tile, int row, int r, uint32_t x) {
+__device__ __forceinline__ void store_quad(uint8_t *tile, int row, int r, const uint32_t (&x)[4]) {
     if constexpr (kPacked) {
-        *reinterpret_cast<uint32_t *>(tile + (r >> 3) * 4096 + sw32_off(row, r & 7)) = x;
+        *reinterpret_cast<uint4 *>(tile + (r >> 3) * 4096 + sw32_off(row, r & 7)) = make_uint4(x[0], x[1], x[2], x[3]);
     } else {
-        *reinterpret_cast<uint16_t *>(tile + sw128_off(row, r)) = (uint16_t)x;
-        *reinterpret_cast<uint16_t *>(tile + sw128_off(row, r + D / 2)) = (uint16_t)(x >> 16);
+        *reinterpret_cast<uint2 *>(tile + sw128_off(row, r)) = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+        *reinterpret_cast<uint2 *>(tile + sw128_off(row, r + D / 2)) = make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
     }
+}
+// The first n words of 32 bytes that lie in two 16-byte units.
+__device__ __forceinline__ void zero_words(uint8_t *u0, uint8_t *u1, int n) {
+    uint8_t *u = n < 4 ? u0 : u1;
+    if (n >= 4) *reinterpret_cast<uint4 *>(u0) = make_uint4(0, 0, 0, 0);
+    if (n & 2) *reinterpret_cast<uint2 *>(u) = make_uint2(0, 0);
+    if (n & 1) *reinterpret_cast<uint32_t *>(u + (n & 2) * 4) = 0;
 }
 // Pairs of one MMA K-step (packed) or of a K-step and its partner (natural).
 template <bool kPacked>
@@ -207,13 +216,10 @@ __device__ __forceinline__ int4 make_band(int r_lo, int r_full, bool spread) {
     return make_int4(r_lo, rs, r_full, flags);
 }
 
-__device__ __forceinline__ int first_kept(const int *w, int H, int64_t d) {
-    int lo = 0, hi = H;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)w[mid] >= d) hi = mid; else lo = mid + 1;
-    }
-    return lo;
+// r*(d) = the smallest r with w_r >= d (H when none), by a warp whose lanes hold the
+// windows of pairs lane and lane + 32 (INT32_MAX past H): the windows do not decrease.
+__device__ __forceinline__ int first_kept(int w0, int w1, int64_t d) {
+    return __popc(__ballot_sync(0xffffffffu, w0 < d)) + __popc(__ballot_sync(0xffffffffu, w1 < d));
 }
 
 // Bounded wait of a whole warp.  The first, suspended attempt covers every wait of
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&ctl->v_empty[s], 1);
             }
             for (int s = 0; s < 2; ++s) {
-                mbar_init(&ctl->s_full[s], 1);
+                mbar_init(&ctl->s_full[s], 2);  // the MMAs, and the issuing warp (for what it has seen of the stage)
                 mbar_init(&ctl->s_read[s], 4);
                 mbar_init(&ctl->p_full[s], 4);
                 mbar_init(&ctl->o_done[s], 1);
@@ -457,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t *full = v ? ctl->v_full : ctl->k_full, *empty = v ? ctl->v_empty : ctl->k_empty;
         const int u = lane >> 1, hf = lane & 1;  // lane = (K-step or dim group, half of the tile)
         const uint32_t P = (uint32_t)a.pk.page_size;
+        const int w0 = w[lane], w1 = H > 32 ? w[lane + 32] : INT32_MAX;
         while (ok && runs.next(wc, ok)) {
             const Segment g = runs.now();
             runs.done(lane);
@@ -475,20 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool issue = hf < (box_keys == kBN ? 1 : halves);
                 const int at = (int)(((uint32_t)m0 + 64u * hf) % P);
                 if (!v) {
-                    // The tile's band.  Over prefix tiles both distances shrink, so the bounds only
-                    // move down; a tile with nodes may hold any small distance.
-                    if (m0 + kBN <= g.L) {
-                        const int64_t dmin = g.pmin - (m0 + kBN - 1), dmax = g.pmax - m0;
-                        if (j == g.tile0) {
-                            r_lo = first_kept(w, H, dmin);
-                            r_full = first_kept(w, H, dmax);
-                        }
-                        while (r_lo > 0 && (int64_t)w[r_lo - 1] >= dmin) --r_lo;
-                        while (r_full > 0 && (int64_t)w[r_full - 1] >= dmax) --r_full;
-                    } else {
-                        r_lo = 0;
-                        r_full = first_kept(w, H, g.pmax - (m0 < g.L ? min(m0, (int64_t)g.kmin) : (int64_t)g.kmin));
-                    }
+                    // The tile's band; a tile with nodes may hold any small distance.
+                    const bool prefix = m0 + kBN <= g.L;
+                    r_lo = prefix ? first_kept(w0, w1, g.pmin - (m0 + kBN - 1)) : 0;
+                    r_full = first_kept(w0, w1, g.pmax - (prefix || (m0 < g.L && m0 < g.kmin) ? m0 : (int64_t)g.kmin));
                 }
                 if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 const int ca = v || !kPacked ? 0 : r_lo >> 3;
@@ -524,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int4 bd = ctl->band[st];
                 if (!(bd.w & kBandFix)) continue;
                 uint8_t *kst = sK + st * F::TileBytes;
+                const bool prefix = m0 + kBN <= g.L;
                 constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
                 int kp[kK];
 #pragma unroll
@@ -532,26 +530,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                     kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
                     if (bd.w & kBandCells) sKpos[st * kBN + lane + 32 * e] = kp[e];
                 }
-                // Pairs below rs that share its K-step are pruned for every cell.
-                for (int r = bd.y / kPer * kPer; r < bd.y; ++r)
+                // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
+                const int z = bd.y % kPer;
+                if (z) {
+                    const int c = bd.y / kPer;
 #pragma unroll
-                    for (int e = 0; e < kK; ++e) store_pair<D, kPacked>(kst, lane + 32 * e, r, 0u);
+                    for (int e = 0; e < kK; ++e) {
+                        if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + 32 * e, 0), kst + c * 4096 + sw32_off(lane + 32 * e, 4), z);
+                        else {
+                            for (int half = 0; half < 2; ++half) {
+                                const int d = 16 * c + half * H;
+                                uint8_t *u0 = kst + sw128_off(lane + 32 * e, d), *u1 = kst + sw128_off(lane + 32 * e, d + 8);
+                                zero_words(u0, u1, z / 2);
+                                if (z & 1) *reinterpret_cast<uint16_t *>((z < 8 ? u0 : u1) + (z & 6) * 2) = 0;
+                            }
+                        }
+                    }
+                }
+                uint32_t chunks = prefix ? 0u : 0xfu;  // 32-key chunks in which some cell is added
+                // Addresses of this lane's first key; its others are 32 rows further each.
+                const uint8_t *row0 = kst + (kPacked ? lane * 32 : lane * 128);
+                const uint32_t swz = kPacked ? (lane & 4) << 2 : (lane & 7) << 4;
                 for (int r = bd.y; r < bd.z; ++r) {
                     // Keys at positions >= all are kept by every row, below none by no row.
                     const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
-                    int z0 = kBN, z1 = 0;
+                    uint32_t *stage = sStage + (st * kStaged + r - bd.y) * kBN + lane;
+                    uint8_t *x0, *x1 = nullptr;
+                    if (kPacked) {
+                        x0 = const_cast<uint8_t *>(row0) + (r >> 3) * 4096 + (((r & 7) * 4) ^ swz);
+                    } else {
+                        x0 = const_cast<uint8_t *>(row0) + (r >> 6) * 16384 + ((((r & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                        x1 = const_cast<uint8_t *>(row0) + ((r + H) >> 6) * 16384 + (((((r + H) & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                    }
 #pragma unroll
                     for (int e = 0; e < kK; ++e) {
-                        const bool some = kp[e] < all && kp[e] >= none;
-                        if (kp[e] < all) {
-                            if (some) sStage[(st * kStaged + r - bd.y) * kBN + lane + 32 * e] = load_pair<D, kPacked>(kst, lane + 32 * e, r);
-                            store_pair<D, kPacked>(kst, lane + 32 * e, r, 0u);
+                        if (kp[e] >= all) continue;
+                        if (kPacked) {
+                            uint32_t *x = reinterpret_cast<uint32_t *>(x0 + e * 1024);
+                            if (kp[e] >= none) stage[32 * e] = *x;
+                            *x = 0;
+                        } else {
+                            uint16_t *lo = reinterpret_cast<uint16_t *>(x0 + e * 4096), *hi = reinterpret_cast<uint16_t *>(x1 + e * 4096);
+                            if (kp[e] >= none) stage[32 * e] = *lo | (uint32_t)*hi << 16;
+                            *lo = 0;
+                            *hi = 0;
                         }
-                        const uint32_t m = __ballot_sync(0xffffffffu, some);
-                        if (m) z0 = min(z0, 32 * e + __ffs(m) - 1), z1 = 32 * e + 32 - __clz(m);
                     }
-                    if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
+                    if (none < all) {
+                        // Staged keys lie in [z0, z1) of a prefix tile, anywhere in one with nodes.
+                        const int z0 = prefix ? (int)min(max(none - m0, (int64_t)0), (int64_t)kBN) : 0;
+                        const int z1 = prefix ? (int)min(max(all - m0, (int64_t)0), (int64_t)kBN) : kBN;
+                        if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
+                        if (z0 < z1) chunks |= (2u << (z1 - 1) / 32) - (1u << z0 / 32);
+                    }
                 }
+                if (lane == 0) ctl->chunks[st] = bd.x < bd.y ? 0xfu : chunks;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
@@ -663,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     umma_commit(&ctl->s_full[set]);
                     umma_commit(&ctl->k_empty[st]);
+                    mbar_arrive(&ctl->s_full[set]);
                 }
                 __syncwarp();
             }
@@ -734,46 +768,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = row < rows;
             const int tok = (row0 + (valid ? row : 0)) / sh.G;
             {
-                // Rotate the queries into the MMA's layout as hi + lo bf16: a thread takes one pair
-                // of every kStep-th row, so neighbouring rows (heads) of a node share its cos and sin.
-                constexpr int kStep = 256 / H;
-                const int pr = threadIdx.x % H;
-                int r = threadIdx.x / H;
-                int t = (row0 + r) / sh.G, hh = (row0 + r) % sh.G, last = -1;
+                // Rotate the queries into the MMA's layout as hi + lo bf16, four pairs of a row per
+                // thread.  A run's first instructions come from L2 a line at a time, so this is a short
+                // loop rather than an unrolled one.
+                constexpr int kQuads = H / 4, kStep = 256 / kQuads;  // threads per row, rows at a time
+                const int pr = threadIdx.x % kQuads * 4;
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + b * a.qs.batch + (int64_t)g.h * sh.G * a.qs.head + pr;
-                float2 cs = make_float2(1.f, 0.f);
+                const ulonglong2 tu01 = *reinterpret_cast<const ulonglong2 *>(&ctl->turn[pr]);
+                const ulonglong2 tu23 = *reinterpret_cast<const ulonglong2 *>(&ctl->turn[pr + 2]);
+                const uint64_t turn[4] = {tu01.x, tu01.y, tu23.x, tu23.y};
+                uint2 xa, xb;
+                int ps = 0;
+                auto fetch = [&](int r) {
+                    if (r >= rows) return;
+                    const int t = (row0 + r) / sh.G, hh = (row0 + r) - t * sh.G;
+                    const __nv_bfloat16 *src = q + t * a.qs.token + hh * a.qs.head;
+                    xa = *reinterpret_cast<const uint2 *>(src);
+                    xb = *reinterpret_cast<const uint2 *>(src + H);
+                    ps = node_pos(a, b, L, t);
+                };
+                int r = threadIdx.x / kQuads;
+                fetch(r);
 #pragma unroll 1
-                for (; r < rows; r += 4 * kStep) {
-                    __nv_bfloat16 xa[4], xb[4];
-                    int ts[4];
+                for (; r < rows; r += kStep) {
+                    const uint2 ya = xa, yb = xb;
+                    const int pos = ps;
+                    fetch(r + kStep);  // under this row's arithmetic
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        ts[u] = t;
-                        if (r + u * kStep < rows) {
-                            const __nv_bfloat16 *src = q + t * a.qs.token + hh * a.qs.head;
-                            xa[u] = src[0];
-                            xb[u] = src[H];
-                        }
-                        hh += kStep;
-                        while (hh >= sh.G) hh -= sh.G, ++t;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t wa = i < 2 ? ya.x : ya.y, wb = i < 2 ? yb.x : yb.y;
+                        const float fa = i & 1 ? bf16hi(wa) : bf16lo(wa), fb = i & 1 ? bf16hi(wb) : bf16lo(wb);
+                        // The hardware's sin and cos (2^-21 on [-pi, pi]) lie far below the 2^-16 of hi + lo.
+                        float sn, cs;
+                        __sincosf((float)(int64_t)((uint64_t)(int64_t)pos * turn[i]) * 3.4061215800865545e-19f, &sn, &cs);
+                        const float x = fa * cs - fb * sn, y = fb * cs + fa * sn;
+                        hi[i] = pack_bf16x2(x, y);
+                        lo[i] = pack_bf16x2(x - bf16lo(hi[i]), y - bf16hi(hi[i]));
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int rr = r + u * kStep;
-                        if (rr >= rows) break;
-                        if (ts[u] != last) {
-                            last = ts[u];
-                            cs = turn_cos_sin(node_pos(a, b, L, last), ctl->turn[pr]);
-                        }
-                        const float fa = __bfloat162float(xa[u]), fb = __bfloat162float(xb[u]);
-                        const float x = fa * cs.x - fb * cs.y, y = fb * cs.x + fa * cs.y;
-                        const uint32_t hi = pack_bf16x2(x, y);
-                        const uint32_t lo = pack_bf16x2(x - bf16lo(hi), y - bf16hi(hi));
-#pragma unroll
-                        for (int cp = 0; cp < kRep; ++cp) {
-                            store_pair<D, kPacked>(sQ, cp * kRows + rr, pr, hi);
-                            store_pair<D, kPacked>(sQ + F::TileBytes, cp * kRows + rr, pr, lo);
-                        }
+                    for (int cp = 0; cp < kRep; ++cp) {
+                        store_quad<D, kPacked>(sQ, cp * kRows + r, pr, hi);
+                        store_quad<D, kPacked>(sQ + F::TileBytes, cp * kRows + r, pr, lo);
                     }
                 }
                 fence_proxy_async_smem();
@@ -789,13 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = j0; j < tile0 + ntile; j += 2) {
                 const int x = it + (j - tile0), st = x % ST;
                 const bool tail = (int64_t)(j + 1) * kBN > L;
-                if (!(ok = wait(&ctl->k_full[st], (x / ST) & 1, wc, 55))) break;
+                if (!(ok = wait(&ctl->s_full[set], (x >> 1) & 1, wc, 56))) break;
+                tc_fence_after();
                 const int4 bd = ctl->band[st];
                 const bool cells = bd.w & kBandCells;
                 __syncwarp();
                 if (!cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);  // nothing of the stage is read here
-                if (!(ok = wait(&ctl->s_full[set], (x >> 1) & 1, wc, 56))) break;
-                tc_fence_after();
                 bool dense = bd.y < H;  // S holds something
                 if (bd.w & kBandFix) {
                     // Waited for only where this warp still holds the stage, so that the barrier
@@ -809,8 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (cells || tail) {
                     // Cells added or hidden, in S itself, 32 columns at a time.
+                    const uint32_t chunks = (cells ? ctl->chunks[st] : 0u) | (tail || !dense ? 0xfu : 0u);
 #pragma unroll 1
                     for (int cc = c0; live && cc < c0 + NC; cc += 32) {
+                        if (!((chunks >> (cc / 32)) & 1u)) continue;
                         uint32_t ra[32];
                         float s[32];
                         __syncwarp();
@@ -827,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + cc);
 #pragma unroll 1
                             for (int r = bd.x; r < bd.z; ++r) {
-                                if (r >= bd.y) {
+                                if (r >= bd.y && !tail) {
                                     const uint32_t z = ctl->zone[st][r - bd.y];
                                     if ((int)(z >> 16) <= cc || (int)(z & 0xffff) >= cc + 32) continue;
                                 }

@@ -56,7 +56,7 @@ CASES = [
                                dict(kwin=math.nan), dict(base=1.0), dict(layout=atf.KV_HND), dict(B=1 << 20, T=1 << 10)]),
     ("tree_decode_paged", -2, [dict(D=96), dict(odt=3)]),
     ("tree_decode_paged", -3, [dict(ws=None), dict(wsb=0)]),
-    ("tree_decode_paged", -6, [dict(q=P + 4), dict(out=P + 2), dict(ws=P + 8), dict(kpages=P + 8)]),
+    ("tree_decode_paged", -6, [dict(q=P + 4), dict(out=P + 2), dict(ws=P + 8), dict(kpages=P + 8), dict(qs=strides(5120, 1028, 128))]),
     ("cache_compact", -1, [dict(kpages=None), dict(vpages=None), dict(bt=None), dict(lens=None), dict(path=None), dict(acc=None), dict(new=P),
                            dict(B=0), dict(M=0), dict(Hkv=0), dict(page=65), dict(layout=atf.KV_HND)]),
     ("cache_compact", -2, [dict(M=1025), dict(D=32)]),
