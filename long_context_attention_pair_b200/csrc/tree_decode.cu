@@ -40,11 +40,10 @@
 // V's own), which moves an output by at most 2^-8 of sum p |v|; sums, maxima and
 // O are fp32.
 //
-// 16 warps: 0-7 softmax (set = warp / 4, TMEM lane quarter warp % 4), 8 K producer,
-// 9 QK issuer, 10 fix-up (stages boundary pairs, zeroes them in K), 11 PV issuer,
-// 12 V producer, 13 scheduler (publishes the runs of tiles through a ring), 14-15
-// tails (mask bits of tiles with nodes, V behind the last node cleared).  Every
-// mbarrier wait is bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its
+// Warps: the softmax warps, then one each for loading K, issuing QK, the fix-up of
+// boundary pairs (staged, and zeroed in K), issuing PV, loading V and scheduling (it
+// publishes the runs of tiles through a ring), and two for the tails (mask bits of
+// tiles with nodes, V behind the last node cleared).  Every mbarrier wait is bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its
 // copies and MMAs finish and exits.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -59,8 +58,8 @@ constexpr int kBM = 128, kBN = 128;
 constexpr int kSoft = 8;
 constexpr int kProducer = 8, kQk = 9, kFix = 10, kPv = 11, kVProducer = 12, kSched = 13, kTail = 14;
 constexpr int kThreads = 32 * 16;
-// Registers: 128 per thread at launch; the last two warpgroups drop to 72 and the
-// two softmax warpgroups rise to 184, within the launch's total (checked here and,
+// Registers: 128 per thread at launch; the last two warpgroups drop to 72 and the two
+// softmax warpgroups rise to 184, within the launch's total (checked here and,
 // against the compiled kernel, at launch).
 constexpr int kLaunchRegs = 128, kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
@@ -143,7 +142,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, const Shape &sh, int b)
     // Slots that the table row has no room for: reported by tree_merge_kernel.
     if (s.L < 0 || s.L + s.nodes > (int64_t)a.pk.max_pages * a.pk.page_size) s.nodes = 0;
     s.tiles = s.nodes ? (int)((s.L + s.nodes + kBN - 1) / kBN) : 0;
-    s.groups = (int)(((int64_t)s.nodes * sh.G + kBM * sh.R - 1) / (kBM * sh.R));
+    s.groups = (int)(((uint32_t)s.nodes * (uint32_t)sh.G + (uint32_t)(kBM * sh.R) - 1u) / (uint32_t)(kBM * sh.R));  // B*T*Hq < 2^31
     return s;
 }
 __device__ __forceinline__ int64_t units_of(const Seq &s, int Hkv) { return (int64_t)Hkv * s.groups * s.tiles; }
@@ -303,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int H = F::H, C = F::C, ST = F::ST;
     constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
     constexpr int kPer = kPairsPerStep<kPacked>;
+    constexpr int CW = NC < 64 ? NC : 64;               // columns in registers at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + F::OffQ, *sK = smem + F::OffK, *sV = smem + F::OffV;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Rotate the queries into the MMA's layout as hi + lo bf16, four pairs of a row per
                 // thread.  A run's first instructions come from L2 a line at a time, so this is a short
                 // loop rather than an unrolled one.
-                constexpr int kQuads = H / 4, kStep = 256 / kQuads;  // threads per row, rows at a time
+                constexpr int kQuads = H / 4, kStep = 32 * kSoft / kQuads;  // threads per row, rows at a time
                 const int pr = threadIdx.x % kQuads * 4;
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + b * a.qs.batch + (int64_t)g.h * sh.G * a.qs.head + pr;
                 const ulonglong2 tu01 = *reinterpret_cast<const ulonglong2 *>(&ctl->turn[pr]);
@@ -913,37 +913,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);
                     if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
                 }
-                // The row's columns, in registers from here on.
-                float s[NC];
-                if (dense) {
-                    // (Loads of 128 columns do not compile for a kernel launched with 128 registers.)
-                    constexpr int kLd = NC == 32 ? 32 : 64;
-                    uint32_t ra[NC / kLd][kLd];
+                // The row's maximum, then the exponentials, CW columns at a time.  Whole rows (NC = 128)
+                // are read twice, by loops: their unrolled code would not stay in the instruction cache.
+                float s[CW], row_max = -INFINITY;
+                auto load = [&](int c) {
+                    if (dense) {
+                        uint32_t ra[CW];
+                        if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + c, ra);
+                        else tmem_ld_32x32b_x32(tS + c, ra);
+                        tmem_ld_wait(ra);
 #pragma unroll
-                    for (int i = 0; i < NC / kLd; ++i) {
-                        if constexpr (kLd == 64) tmem_ld_32x32b_x64(tS + c0 + 64 * i, ra[i]);
-                        else tmem_ld_32x32b_x32(tS + c0, ra[i]);
+                        for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CW; ++i) s[i] = 0.f;
                     }
+                };
+                auto s_free = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->s_read[set]);
+                };
+#pragma unroll 1
+                for (int c = c0; c < c0 + NC; c += CW) {
+                    load(c);
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < NC / kLd; ++i) tmem_ld_wait(ra[i]);
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) s[i] = __uint_as_float(ra[i / kLd][i % kLd]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) s[i] = 0.f;
+                    for (int i = 0; i < CW; i += 8) {
+                        row_max = max3(row_max, s[i], s[i + 1]);
+                        mx0 = max3(mx0, s[i + 2], s[i + 3]);
+                        mx1 = max3(mx1, s[i + 4], s[i + 5]);
+                        mx2 = max3(mx2, s[i + 6], s[i + 7]);
+                    }
+                    row_max = fmaxf(fmaxf(row_max, mx0), fmaxf(mx1, mx2));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->s_read[set]);
-                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < NC; i += 8) {
-                    mx0 = max3(mx0, s[i], s[i + 1]);
-                    mx1 = max3(mx1, s[i + 2], s[i + 3]);
-                    mx2 = max3(mx2, s[i + 4], s[i + 5]);
-                    mx3 = max3(mx3, s[i + 6], s[i + 7]);
-                }
-                const float tile_max = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale_log2;
+                if (NC == CW) s_free();
+                const float tile_max = row_max * scale_log2;
                 // The running max after the previous tile, from the row's warp of the other set.  It is
                 // kept unless it grew by more than 2^8: O / l uses the same one, so the result does not
                 // depend on it.
@@ -968,40 +973,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                 }
                 if (live) {
+#pragma unroll 1
+                    for (int c = c0; c < c0 + NC; c += CW) {
+                        if (NC > CW) load(c);
 #pragma unroll
-                    for (int q = 0; q < NC; q += 32) {
-                        uint32_t pk[16];
+                        for (int q = 0; q < CW; q += 32) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float2 xa = fma2(make_float2(s[q + 2 * i], s[q + 2 * i + 1]), sc2, mneg);
-                            float2 xb = fma2(make_float2(s[q + 2 * i + 2], s[q + 2 * i + 3]), sc2, mneg);
-                            xa.x = fast_exp2(xa.x);
-                            xa.y = fast_exp2(xa.y);
-                            xb.x = fast_exp2(xb.x);
-                            xb.y = fast_exp2(xb.y);
-                            l0 = add2(l0, xa);
-                            l1 = add2(l1, xb);
-                            pk[i] = pack_bf16x2(xa.x, xa.y);
-                            pk[i + 1] = pack_bf16x2(xb.x, xb.y);
+                            for (int i = 0; i < 16; i += 2) {
+                                float2 xa = fma2(make_float2(s[q + 2 * i], s[q + 2 * i + 1]), sc2, mneg);
+                                float2 xb = fma2(make_float2(s[q + 2 * i + 2], s[q + 2 * i + 3]), sc2, mneg);
+                                xa.x = fast_exp2(xa.x);
+                                xa.y = fast_exp2(xa.y);
+                                xb.x = fast_exp2(xb.x);
+                                xb.y = fast_exp2(xb.y);
+                                l0 = add2(l0, xa);
+                                l1 = add2(l1, xb);
+                                pk[i] = pack_bf16x2(xa.x, xa.y);
+                                pk[i + 1] = pack_bf16x2(xb.x, xb.y);
+                            }
+                            tmem_st_x16(tP + (c + q) / 2, pk);
                         }
-                        tmem_st_x16(tP + (c0 + q) / 2, pk);
                     }
                     const float2 ls = add2(l0, l1);
                     lrun += ls.x + ls.y;
                 }
+                if (NC > CW) s_free();
                 if (j > tile0 && __any_sync(0xffffffffu, need)) {
                     // O may be rescaled once the previous tile's PV is done.
                     if (!(ok = wait(&ctl->o_done[set ^ 1], ((x - 1) >> 1) & 1, wc, 64))) break;
                     tc_fence_after();
                     const float alpha = need ? fast_exp2(m_prev - m_new) : 1.f;
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 32; ++cc) {
+                    for (int cc = 0; cc < D; cc += 32) {
                         uint32_t r[32];
-                        tmem_ld_32x32b_x32(tO + cc * 32, r);
+                        tmem_ld_32x32b_x32(tO + cc, r);
                         tmem_ld_wait(r);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                        tmem_st_32x32b_x32(tO + cc * 32, r);
+                        tmem_st_32x32b_x32(tO + cc, r);
                     }
                 }
                 tmem_st_wait();
@@ -1051,16 +1061,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kO = D / 2;
             float *sX = reinterpret_cast<float *>(sQ);  // exchange of repeated rows: every QK of the run is done
 #pragma unroll 1
-            for (int cc = 0; cc < kO / 32; ++cc) {
-                const int d0 = set * kO + cc * 32;
+            for (int cc = 0; cc < kO; cc += 32) {
+                const int d0 = set * kO + cc;
                 uint32_t ra[32];
                 __syncwarp();
                 tmem_ld_32x32b_x32(tO + d0, ra);
                 tmem_ld_wait(ra);
                 float o[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = kRep > 1 ? __uint_as_float(ra[i]) * f : __uint_as_float(ra[i]);
+                for (int i = 0; i < 32; ++i) o[i] = kRep > 1 ? __uint_as_float(ra[i]) * f : __uint_as_float(ra[i]);
                 if (odd && valid && copy == 0) {
                     float t[32];  // (in local memory, only here)
 #pragma unroll
@@ -1072,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kRep > 1) {
                     // Rows of float4 units, the unit index swizzled by the row against bank conflicts.
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 32 / 4; ++i) {
                         const int unit = (d0 / 4 + i) ^ (lane & 7);
                         *reinterpret_cast<float4 *>(sX + (q4 * 32 + lane) * D + unit * 4) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
@@ -1080,18 +1089,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!whole) {
                         float4 *dst = reinterpret_cast<float4 *>(part + 2 * kBM + (size_t)row * D + d0);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 32 / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     } else {
                         const size_t orow = (obase + tok) * a.Hq + g.h * sh.G + (row0 + row) % sh.G;
                         if (a.out_f32) {
                             float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D + d0);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
+                            for (int i = 0; i < 32 / 4; ++i)
                                 dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
                         } else {
                             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + d0);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 32 / 8; ++i)
                                 dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                                     pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                         }
@@ -1102,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (set == 0 && copy == 0) ctl->run_max[0][row] = inv;  // for the threads that write the row
                 if (!(ok = soft_sync())) break;
                 // Copies summed, a float4 unit at a time, neighbouring threads on neighbouring units.
-                for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
+                for (int e = threadIdx.x; e < rows * (D / 4); e += 32 * kSoft) {
                     const int r = e / (D / 4), u = e % (D / 4);
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1150,9 +1159,10 @@ template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Shape sh) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const bool exists = id < (int64_t)a.B * a.T * a.Hq;
-    const int hq = (int)(id % a.Hq), i = (int)(id / a.Hq % a.T), b = exists ? (int)(id / a.Hq / a.T) : 0;
+    const int64_t id64 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const bool exists = id64 < (int64_t)a.B * a.T * a.Hq;
+    const int id = exists ? (int)id64 : 0;  // rows fit 31 bits
+    const int hq = id % a.Hq, i = id / a.Hq % a.T, b = id / a.Hq / a.T;
     const Seq s = seq_of(a, sh, b);
     const int64_t before = units_before(a, sh, b), total = units_before(a, sh, sh.B);
     if (exists && i == 0 && hq == 0 && lane == 0) {
@@ -1166,7 +1176,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     const int64_t first = before + ((int64_t)h * s.groups + rt / sh.R) * s.tiles;
     const int active = active_groups(total, sh.groups);
     // Group of unit x: the largest g with floor(g * total / active) <= x.
-    const int g0 = (int)(((first + 1) * active - 1) / total), g1 = (int)(((first + s.tiles) * active - 1) / total);
+    const auto group_of = [&](int64_t x) {
+        const int64_t y = (x + 1) * active - 1;
+        return (int)((y | total) >> 31 ? y / total : (uint32_t)y / (uint32_t)total);
+    };
+    const int g0 = group_of(first), g1 = group_of(first + s.tiles - 1);
     if (g0 == g1) return;
     const int row = r % kBM;
     auto state = [&](int g) {
