@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int H = F::H, C = F::C, ST = F::ST;
     constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
     constexpr int kPer = kPairsPerStep<kPacked>;
-    constexpr int CW = NC < 64 ? NC : 64;               // columns in registers at a time
+    constexpr int CW = NC < 32 ? NC : 32;              // columns in registers at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + F::OffQ, *sK = smem + F::OffK, *sV = smem + F::OffV;
