@@ -221,13 +221,20 @@ __device__ __forceinline__ int first_kept(int w0, int w1, int64_t d) {
     return __popc(__ballot_sync(0xffffffffu, w0 < d)) + __popc(__ballot_sync(0xffffffffu, w1 < d));
 }
 
-// Bounded wait of a whole warp.  The first, suspended attempt covers every wait of
-// a healthy pipeline without reading the (slow) global timer.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, WaitCtl &wc, uint32_t site) {
-    bool ok = mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 20000u);
+// Bounded wait of a whole warp.  Short, for the instruction cache's sake; the (slow)
+// global timer is first read after a whole suspended attempt.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const WaitCtl &wc, uint32_t site) {
+    bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
-        wc.site = site;
-        ok = mbar_wait(bar, parity, wc);
+        uint64_t t0 = 0, now = 0;
+        while (!(ok = mbar_try_wait_sleep(bar, parity, 20000u)) && !*wc.abort_flag && now - t0 <= wc.limit_ns) {
+            now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+        }
+        if (!ok) {
+            *wc.abort_flag = 1;
+            atomicCAS(wc.status, 0, ATFLASH_DEVICE_TIMEOUT_BASE + (int)site);
+        }
     }
     return __all_sync(0xffffffffu, ok);
 }
