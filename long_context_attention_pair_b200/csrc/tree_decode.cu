@@ -66,6 +66,7 @@ static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "reg
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
 constexpr int kStaged = 16;      // boundary pairs staged per tile (at least one natural K-step)
+constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
@@ -86,8 +87,9 @@ struct Cfg {
     static constexpr int CtlBytes = 6144;
     static constexpr int Request = OffCtl + CtlBytes + 1024;
     static_assert(Request <= 232448, "shared memory of one CTA");
-    // TMEM: S of set t at 128 t, P (64 columns of bf16 pairs) at 256 + 64 t, O at 384.
-    static constexpr uint32_t TmemP = 256, TmemO = 384, TmemCols = 512;
+    // TMEM: S of a tile in one of three buffers at 0, 128 and 256, its P (64 columns of bf16 pairs)
+    // over the columns of S that have been read, O at 384.
+    static constexpr uint32_t TmemO = 384, TmemCols = 512;
 };
 
 // One run of key tiles of one item.
@@ -104,7 +106,7 @@ struct Ctl {
     uint64_t seg_full[kRing], seg_empty[kRing];
     uint64_t q_ready;
     uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-    uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
+    uint64_t s_full[kBufs], p_full[kBufs], o_done[kBufs];  // per S / P buffer
     uint64_t m_full[2], m_empty[2];
     uint64_t max_bar[2][4];          // per set and lane quarter: the running max after its tile is posted
     uint64_t drain, soft_bar;
@@ -337,11 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&ctl->v_ready[s], 2);
                 mbar_init(&ctl->v_empty[s], 1);
             }
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < kBufs; ++s) {
                 mbar_init(&ctl->s_full[s], 2);  // the MMAs, and the issuing warp (for what it has seen of the stage)
-                mbar_init(&ctl->s_read[s], 4);
                 mbar_init(&ctl->p_full[s], 4);
                 mbar_init(&ctl->o_done[s], 1);
+            }
+            for (int s = 0; s < 2; ++s) {
                 mbar_init(&ctl->m_full[s], 2);
                 mbar_init(&ctl->m_empty[s], 4);
                 for (int q = 0; q < 4; ++q) mbar_init(&ctl->max_bar[s][q], 1);
@@ -672,17 +675,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             runs.done(lane);
             if (!(ok = wait(&ctl->q_ready, (runs.n - 1) & 1, wc, 46))) break;
             for (int j = 0; ok && j < ntile; ++j, ++it) {
-                const int st = it % ST, set = it & 1;
+                const int st = it % ST, buf = it % kBufs;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
                 const int4 bd = ctl->band[st];
                 if (bd.w & kBandFix) {
                     if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
                     fixed ^= 1u << st;
                 }
-                if (it >= 2 && !(ok = wait(&ctl->s_read[set], ((it >> 1) - 1) & 1, wc, 49))) break;
+                if (it >= kBufs && !(ok = wait(&ctl->o_done[buf], (it / kBufs - 1) & 1, wc, 49))) break;
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + set * kBN;
+                    const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + buf * kBN;
                     uint32_t acc = 0;
                     for (int c = bd.y / kPer; c < H / kPer; ++c) {
 #pragma unroll
@@ -701,9 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    umma_commit(&ctl->s_full[set]);
+                    umma_commit(&ctl->s_full[buf]);
                     umma_commit(&ctl->k_empty[st]);
-                    mbar_arrive(&ctl->s_full[set]);
+                    mbar_arrive(&ctl->s_full[buf]);
                 }
                 __syncwarp();
             }
@@ -717,21 +720,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int L = runs.now().L, tile0 = runs.now().tile0, ntile = runs.now().ntile;
             runs.done(lane);
             for (int j = tile0; ok && j < tile0 + ntile; ++j, ++it) {
-                const int st = it % ST, set = it & 1;
+                const int st = it % ST, buf = it % kBufs;
                 if (!(ok = wait(&ctl->v_full[st], (it / ST) & 1, wc, 50))) break;
                 if ((int64_t)(j + 1) * kBN > L) {
                     if (!(ok = wait(&ctl->v_ready[st], (tails >> st) & 1, wc, 51))) break;
                     tails ^= 1u << st;
                 }
-                if (!(ok = wait(&ctl->p_full[set], (it >> 1) & 1, wc, 52))) break;
+                if (!(ok = wait(&ctl->p_full[buf], (it / kBufs) & 1, wc, 52))) break;
                 if (lane == 0) {
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk) {
                         const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
-                        umma_bf16_ts(tmem + F::TmemO, tmem + F::TmemP + set * 64 + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
+                        umma_bf16_ts(tmem + F::TmemO, tmem + buf * kBN + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
                     }
-                    umma_commit(&ctl->o_done[set]);
+                    umma_commit(&ctl->o_done[buf]);
                     umma_commit(&ctl->v_empty[st]);
                 }
                 __syncwarp();
@@ -745,8 +748,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = copy * NC;
         const int row = (q4 * 32) % kRows + lane;        // row of the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const uint32_t tS = tmem + set * kBN + lane_off;
-        const uint32_t tP = tmem + F::TmemP + set * 64 + lane_off;
         const uint32_t tO = tmem + F::TmemO + lane_off;
         const float scale_log2 = 1.4426950408889634f * rsqrtf((float)D);
         uint32_t fixed = 0;                              // phase bit of k_ready per stage
@@ -757,17 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&ctl->soft_bar);
             return wait(&ctl->soft_bar, syncs++ & 1, wc, 53);
         };
-        if (kRep > 1) {
-            // P is zero in the other copies' columns for good.
-            uint32_t zero[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) zero[i] = 0;
-#pragma unroll
-            for (int i = 0; i < kRep; ++i)
-                if (i != copy)
-                    for (int x = 0; x < NC / 32; ++x) tmem_st_x16(tP + i * (NC / 2) + 16 * x, zero);
-            tmem_st_wait();
-        }
         while (ok && runs.next(wc, ok)) {
             const Segment &g = runs.now();
             const int rows = g.rows, row0 = g.row0, b = g.b, L = g.L, tile0 = g.tile0, ntile = g.ntile;
@@ -830,9 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pmax = g.pmax;
             const int j0 = tile0 + ((it ^ set) & 1);  // this set's tiles
             for (int j = j0; j < tile0 + ntile; j += 2) {
-                const int x = it + (j - tile0), st = x % ST;
+                const int x = it + (j - tile0), st = x % ST, buf = x % kBufs;
+                const uint32_t tS = tmem + buf * kBN + lane_off;  // S, and P over it
                 const bool tail = (int64_t)(j + 1) * kBN > L;
-                if (!(ok = wait(&ctl->s_full[set], (x >> 1) & 1, wc, 56))) break;
+                if (!(ok = wait(&ctl->s_full[buf], (x / kBufs) & 1, wc, 56))) break;
                 tc_fence_after();
                 const int4 bd = ctl->band[st];
                 const bool cells = bd.w & kBandCells;
@@ -936,11 +927,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < CW; ++i) s[i] = 0.f;
                     }
                 };
-                auto s_free = [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->s_read[set]);
-                };
 #pragma unroll 1
                 for (int c = c0; c < c0 + NC; c += CW) {
                     load(c);
@@ -954,7 +940,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     row_max = fmaxf(fmaxf(row_max, mx0), fmaxf(mx1, mx2));
                 }
-                if (NC == CW) s_free();
                 const float tile_max = row_max * scale_log2;
                 // The running max after the previous tile, from the row's warp of the other set.  It is
                 // kept unless it grew by more than 2^8: O / l uses the same one, so the result does not
@@ -974,11 +959,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mr = m_new == -INFINITY ? 0.f : m_new;  // nothing seen so far
                 const float2 mneg = make_float2(-mr, -mr), sc2 = make_float2(scale_log2, scale_log2);
                 float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-                // P of this set is free once its previous PV is done.
-                if (x >= 2) {
-                    if (!(ok = wait(&ctl->o_done[set], ((x >> 1) - 1) & 1, wc, 61))) break;
-                    tc_fence_after();
-                }
                 if (live) {
 #pragma unroll 1
                     for (int c = c0; c < c0 + NC; c += CW) {
@@ -999,16 +979,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pk[i] = pack_bf16x2(xa.x, xa.y);
                                 pk[i + 1] = pack_bf16x2(xb.x, xb.y);
                             }
-                            tmem_st_x16(tP + (c + q) / 2, pk);
+                            tmem_st_x16(tS + (c + q) / 2, pk);
                         }
+                    }
+                    if (kRep > 1) {
+                        // P is zero in the other copies' columns.
+                        uint32_t zero[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll 1
+                        for (int c = 0; c < kBN / 2; c += 16)
+                            if (c / (NC / 2) != copy) tmem_st_x16(tS + c, zero);
                     }
                     const float2 ls = add2(l0, l1);
                     lrun += ls.x + ls.y;
                 }
-                if (NC > CW) s_free();
                 if (j > tile0 && __any_sync(0xffffffffu, need)) {
                     // O may be rescaled once the previous tile's PV is done.
-                    if (!(ok = wait(&ctl->o_done[set ^ 1], ((x - 1) >> 1) & 1, wc, 64))) break;
+                    if (!(ok = wait(&ctl->o_done[(x - 1) % kBufs], ((x - 1) / kBufs) & 1, wc, 64))) break;
                     tc_fence_after();
                     const float alpha = need ? fast_exp2(m_prev - m_new) : 1.f;
 #pragma unroll 1
@@ -1024,13 +1012,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->p_full[set]);
+                if (lane == 0) mbar_arrive(&ctl->p_full[buf]);
             }
             if (!ok) break;
             it += ntile;
             // ---- end of the run: the sets' sums and the copies' states of each row joined
             const int lastx = it - 1 - ((it - 1 - set) & 1);  // this set's last tile
-            if (j0 < tile0 + ntile && !(ok = wait(&ctl->o_done[set], (lastx >> 1) & 1, wc, 62))) break;
+            if (j0 < tile0 + ntile && !(ok = wait(&ctl->o_done[lastx % kBufs], (lastx / kBufs) & 1, wc, 62))) break;
             ctl->stat[set][q4 * 32 + lane] = make_float2(m_used, lrun);
             if (!(ok = soft_sync())) break;  // both sets' sums, and O
             tc_fence_after();
