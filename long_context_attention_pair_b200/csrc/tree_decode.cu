@@ -113,7 +113,8 @@ struct Ctl {
     uint32_t tmem_base;
     int abort_flag;
     Segment seg[kRing];
-    int4 band[4];                    // of the tile in each stage: (r_lo, rs, r_full, flags), see Band
+    int4 band[8];                    // of tile it in entry it % 8: (r_lo, rs, r_full, flags), see make_band.  (A tile's
+                                     // entry is rewritten only after its PV, hence after every reader.)
     uint32_t chunks[4];              // 32-key chunks of the tile in which cells are added
     uint32_t zone[4][kStaged];       // of staged pair rs + i: first key and end of the keys added per cell
     int nf_seg[8];                   // run (mod 8) whose tree holds a non-finite value
@@ -239,6 +240,9 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const WaitC
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = globaltimer_ns();
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 const int ca = v || !kPacked ? 0 : r_lo >> 3;
                 if (lane == 0) {
-                    if (!v) ctl->band[st] = make_band<kPacked>(r_lo, r_full, g.pmin != g.pmax);
+                    if (!v) ctl->band[it % 8] = make_band<kPacked>(r_lo, r_full, g.pmin != g.pmax);
                     mbar_expect_tx(&full[st], (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves);
                 }
                 __syncwarp();
@@ -528,18 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = it % ST;
                 const int64_t m0 = (int64_t)j * kBN;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
-                const int4 bd = ctl->band[st];
+                const int4 bd = ctl->band[it % 8];
                 if (!(bd.w & kBandFix)) continue;
                 uint8_t *kst = sK + st * F::TileBytes;
-                const bool prefix = m0 + kBN <= g.L;
                 constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
-                int kp[kK];
-#pragma unroll
-                for (int e = 0; e < kK; ++e) {
-                    const int64_t slot = m0 + lane + 32 * e;
-                    kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
-                    if (bd.w & kBandCells) sKpos[st * kBN + lane + 32 * e] = kp[e];
-                }
                 // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
                 const int z = bd.y % kPer;
                 if (z) {
@@ -557,44 +553,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                uint32_t chunks = prefix ? 0u : 0xfu;  // 32-key chunks in which some cell is added
-                // Addresses of this lane's first key; its others are 32 rows further each.
-                const uint8_t *row0 = kst + (kPacked ? lane * 32 : lane * 128);
-                const uint32_t swz = kPacked ? (lane & 4) << 2 : (lane & 7) << 4;
-                for (int r = bd.y; r < bd.z; ++r) {
-                    // Keys at positions >= all are kept by every row, below none by no row.
-                    const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
-                    uint32_t *stage = sStage + (st * kStaged + r - bd.y) * kBN + lane;
-                    uint8_t *x0, *x1 = nullptr;
-                    if (kPacked) {
-                        x0 = const_cast<uint8_t *>(row0) + (r >> 3) * 4096 + (((r & 7) * 4) ^ swz);
-                    } else {
-                        x0 = const_cast<uint8_t *>(row0) + (r >> 6) * 16384 + ((((r & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
-                        x1 = const_cast<uint8_t *>(row0) + ((r + H) >> 6) * 16384 + (((((r + H) & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
-                    }
+                if (bd.x < bd.z) {
+                    const bool prefix = m0 + kBN <= g.L;
+                    int kp[kK];
 #pragma unroll
                     for (int e = 0; e < kK; ++e) {
-                        if (kp[e] >= all) continue;
+                        const int64_t slot = m0 + lane + 32 * e;
+                        kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
+                        if (bd.w & kBandCells) sKpos[st * kBN + lane + 32 * e] = kp[e];
+                    }
+                    uint32_t chunks = prefix ? 0u : 0xfu;  // 32-key chunks in which some cell is added
+                    // Addresses of this lane's first key; its others are 32 rows further each.
+                    const uint8_t *row0 = kst + (kPacked ? lane * 32 : lane * 128);
+                    const uint32_t swz = kPacked ? (lane & 4) << 2 : (lane & 7) << 4;
+                    for (int r = bd.y; r < bd.z; ++r) {
+                        // Keys at positions >= all are kept by every row, below none by no row.
+                        const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
+                        uint32_t *stage = sStage + (st * kStaged + r - bd.y) * kBN + lane;
+                        uint8_t *x0, *x1 = nullptr;
                         if (kPacked) {
-                            uint32_t *x = reinterpret_cast<uint32_t *>(x0 + e * 1024);
-                            if (kp[e] >= none) stage[32 * e] = *x;
-                            *x = 0;
+                            x0 = const_cast<uint8_t *>(row0) + (r >> 3) * 4096 + (((r & 7) * 4) ^ swz);
                         } else {
-                            uint16_t *lo = reinterpret_cast<uint16_t *>(x0 + e * 4096), *hi = reinterpret_cast<uint16_t *>(x1 + e * 4096);
-                            if (kp[e] >= none) stage[32 * e] = *lo | (uint32_t)*hi << 16;
-                            *lo = 0;
-                            *hi = 0;
+                            x0 = const_cast<uint8_t *>(row0) + (r >> 6) * 16384 + ((((r & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                            x1 = const_cast<uint8_t *>(row0) + ((r + H) >> 6) * 16384 + (((((r + H) & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                        }
+#pragma unroll
+                        for (int e = 0; e < kK; ++e) {
+                            if (kp[e] >= all) continue;
+                            if (kPacked) {
+                                uint32_t *x = reinterpret_cast<uint32_t *>(x0 + e * 1024);
+                                if (kp[e] >= none) stage[32 * e] = *x;
+                                *x = 0;
+                            } else {
+                                uint16_t *lo = reinterpret_cast<uint16_t *>(x0 + e * 4096), *hi = reinterpret_cast<uint16_t *>(x1 + e * 4096);
+                                if (kp[e] >= none) stage[32 * e] = *lo | (uint32_t)*hi << 16;
+                                *lo = 0;
+                                *hi = 0;
+                            }
+                        }
+                        if (none < all) {
+                            // Staged keys lie in [z0, z1) of a prefix tile, anywhere in one with nodes.
+                            const int z0 = prefix ? (int)min(max(none - m0, (int64_t)0), (int64_t)kBN) : 0;
+                            const int z1 = prefix ? (int)min(max(all - m0, (int64_t)0), (int64_t)kBN) : kBN;
+                            if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
+                            if (z0 < z1) chunks |= (2u << (z1 - 1) / 32) - (1u << z0 / 32);
                         }
                     }
-                    if (none < all) {
-                        // Staged keys lie in [z0, z1) of a prefix tile, anywhere in one with nodes.
-                        const int z0 = prefix ? (int)min(max(none - m0, (int64_t)0), (int64_t)kBN) : 0;
-                        const int z1 = prefix ? (int)min(max(all - m0, (int64_t)0), (int64_t)kBN) : kBN;
-                        if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
-                        if (z0 < z1) chunks |= (2u << (z1 - 1) / 32) - (1u << z0 / 32);
-                    }
+                    if (lane == 0) ctl->chunks[st] = bd.x < bd.y ? 0xfu : chunks;
                 }
-                if (lane == 0) ctl->chunks[st] = bd.x < bd.y ? 0xfu : chunks;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; ok && j < ntile; ++j, ++it) {
                 const int st = it % ST, buf = it % kBufs;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
-                const int4 bd = ctl->band[st];
+                const int4 bd = ctl->band[it % 8];
                 if (bd.w & kBandFix) {
                     if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
                     fixed ^= 1u << st;
@@ -707,6 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(&ctl->s_full[buf]);
                     umma_commit(&ctl->k_empty[st]);
                     mbar_arrive(&ctl->s_full[buf]);
+                    // The softmax warps read the stage only where cells are added; otherwise their
+                    // arrivals are made here.
+                    if (!(bd.w & kBandCells)) mbar_arrive_n(&ctl->k_empty[st], 4);
                 }
                 __syncwarp();
             }
@@ -825,10 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool tail = (int64_t)(j + 1) * kBN > L;
                 if (!(ok = wait(&ctl->s_full[buf], (x / kBufs) & 1, wc, 56))) break;
                 tc_fence_after();
-                const int4 bd = ctl->band[st];
+                const int4 bd = ctl->band[x % 8];
                 const bool cells = bd.w & kBandCells;
-                __syncwarp();
-                if (!cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);  // nothing of the stage is read here
                 bool dense = bd.y < H;  // S holds something
                 if (bd.w & kBandFix) {
                     // Waited for only where this warp still holds the stage, so that the barrier
