@@ -456,72 +456,87 @@ def decode(q, k_cache, v_cache, seqlens, rope_base: float, k_window: float = mat
     return out
 
 
-def _strided(t, name, B, T, heads, D, dtype, written=False):
-    """Pointer and host strides {batch, token, head} of a [B, T, heads, D] tensor whose dims are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (B, T, heads, D):
-        raise ValueError(f"{name} must be [{B}, {T}, {heads}, {D}], got {tuple(t.shape)}")
+def _device_of(*tensors):
+    """Index of the one CUDA device that holds every tensor given (None entries skipped)."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("tensors must be CUDA tensors")
+                if dev is not None:
+                    raise ValueError(f"all tensors must be on one device, got cuda:{dev} and cuda:{d}")
+                dev = d
+    return dev
+
+
+def _launch(fn, name, dev, stream, fresh, *args):
+    """fn(*args, stream) with ``dev`` current.  ``fresh``: tensors allocated for this call on
+    the current stream, kept reserved until ``stream`` is done with them."""
+    torch = _torch()
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is not None and stream.cuda_stream != raw:
+        raw = stream.cuda_stream
+        for t in fresh:
+            if t is not None:
+                t.record_stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != OK:
+        raise AtflashError(status, name)
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _strided(t, name, shape, dtype, written=False):
+    """Address and host strides {batch, token, head} of a [B, T, heads, D] tensor whose dims are
+    contiguous (None, meaning contiguous, where the whole tensor is)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
     strides = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]  # of a dimension of one, nothing depends on it
     if strides[3] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     if written and any(s == 0 and n > 1 for n, s in zip(t.shape, strides)):
         raise ValueError(f"{name} is written and must not be an expanded tensor")
-    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*strides[:3])
+    return t.data_ptr(), _Strides(*strides[:3])
 
 
-def _ints(t, name, shape):
-    """Pointer of a contiguous int32 CUDA tensor of the given shape, or None."""
+def _flat(t, name, shape, dtype):
+    """Address of a contiguous tensor of the given shape and type; None for None."""
     if t is None:
         return None
-    if t.dtype != _torch().int32:
-        raise TypeError(f"{name} must be int32")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
-    return _dev(t, name)
-
-
-def _same_device(*tensors):
-    """The one CUDA device of the tensors given, as a context that makes it current."""
-    torch = _torch()
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    return torch.cuda.device(dev)
-
-
-def _on_stream(stream, *fresh):
-    """Tensors allocated for this call stay reserved until ``stream`` is done with them."""
-    if stream is not None and stream != _torch().cuda.current_stream():
-        for t in fresh:
-            if t is not None:
-                t.record_stream(stream)
-    return _stream_ptr(stream)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _pools(kpages, vpages, page_size, kv_layout, dtype):
-    """(layout code, Hkv, D, num_pages) of a paged cache after checking its shapes."""
-    lay = {"NHD": KV_NHD, "PACKED": KV_PACKED}.get(kv_layout)
-    if lay is None:
+    """(layout code, Hkv, D, num_pages, address of K, of V) of a paged cache after checking its shapes."""
+    if kv_layout != "NHD" and kv_layout != "PACKED":
         raise ValueError("kv_layout must be 'NHD' or 'PACKED'")
     num_pages, P, Hkv, D = vpages.shape
     if P != page_size:
         raise ValueError(f"vpages must hold pages of page_size = {page_size} tokens, got {P}")
-    want = (num_pages, P, Hkv, D) if lay == KV_NHD else (num_pages, Hkv, D // 16, P, 16)
-    if tuple(kpages.shape) != want:
-        raise ValueError(f"kpages must be {list(want)} for kv_layout {kv_layout!r}, got {tuple(kpages.shape)}")
-    if kpages.dtype != dtype or vpages.dtype != dtype:
-        raise TypeError("kpages and vpages must be bfloat16")
-    return lay, Hkv, D, num_pages
+    want = (num_pages, P, Hkv, D) if kv_layout == "NHD" else (num_pages, Hkv, D // 16, P, 16)
+    return (KV_NHD if kv_layout == "NHD" else KV_PACKED, Hkv, D, num_pages, _flat(kpages, "kpages", want, dtype),
+            _flat(vpages, "vpages", vpages.shape, dtype))
 
 
 def _rope_arg(name, rope_base, theta, dims):
-    """The C call (base or frequency table) and its frequency argument."""
+    """The C call (base or frequency table), its name and its frequency argument."""
     if theta is None:
         return getattr(lib(), name), name, float(rope_base)
     return getattr(lib(), name + "_theta"), name + "_theta", _theta_arg(theta, dims)
@@ -541,26 +556,29 @@ def rope_apply(q, k, positions, rope_base: float, *, rotary_dim=None, interleave
     """
     torch = _torch()
     B, T, Hq, D = q.shape
-    Hkv = k.shape[2] if k is not None else 0
+    dt, dtype = _dtype_code(q), q.dtype
+    dev = _device_of(q, k, positions, out_q, out_k)
+    fresh = (None, None)
+    if out_q is None or (k is not None and out_k is None):
+        new_q = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device) if out_q is None else None
+        new_k = torch.empty(k.shape, dtype=dtype, device=q.device) if k is not None and out_k is None else None
+        fresh = (new_q, new_k)
+        out_q, out_k = (out_q if new_q is None else new_q), (out_k if new_k is None else new_k)
+    shape = (B, T, Hq, D)
+    qp, qs = _strided(q, "q", shape, dtype)
+    oqp, oqs = _strided(out_q, "out_q", shape, dtype, True)
+    kp = ks = okp = oks = None
+    Hkv = 0
+    if k is not None:
+        Hkv = k.shape[2]
+        shape = (B, T, Hkv, D)
+        kp, ks = _strided(k, "k", shape, dtype)
+        okp, oks = _strided(out_k, "out_k", shape, dtype, True)
     R = D if rotary_dim is None else int(rotary_dim)
-    dt = _dtype_code(q)
-    new_q, new_k = out_q is None, out_k is None and k is not None
-    with _same_device(q, k, positions, out_q, out_k):
-        pos = _ints(positions, "positions", (B, T))
-        qp, qs = _strided(q, "q", B, T, Hq, D, q.dtype)
-        if new_q:
-            out_q = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
-        oqp, oqs = _strided(out_q, "out_q", B, T, Hq, D, q.dtype, True)
-        kp = ks = okp = oks = None
-        if k is not None:
-            kp, ks = _strided(k, "k", B, T, Hkv, D, q.dtype)
-            if new_k:
-                out_k = torch.empty((B, T, Hkv, D), dtype=q.dtype, device=q.device)
-            okp, oks = _strided(out_k, "out_k", B, T, Hkv, D, q.dtype, True)
-        fn, name, rope = _rope_arg("atflash_rope_apply", rope_base, theta, R)
-        sp = _on_stream(stream, out_q if new_q else None, out_k if new_k else None)
-        _check(fn(qp, qs, kp, ks, oqp, oqs, okp, oks, pos, B, T, Hq, Hkv, D, R, rope, float(scale), int(bool(interleaved)),
-                  int(bool(inverse)), dt, sp), name)
+    fn, name, rope = _rope_arg("atflash_rope_apply", rope_base, theta, R)
+    _launch(fn, name, dev, stream, fresh, qp, qs, kp, ks, oqp, oqs, okp, oks,
+            _flat(positions, "positions", (B, T), torch.int32), B, T, Hq, Hkv, D, R, rope, float(scale),
+            int(bool(interleaved)), int(bool(inverse)), dt)
     return out_q if k is None else (out_q, out_k)
 
 
@@ -576,17 +594,19 @@ def cache_append(k, v, kpages, vpages, block_table, seqlens, page_size: int, rop
     """
     torch = _torch()
     B, T, Hkv, D = k.shape
-    with _same_device(k, v, kpages, vpages, block_table, seqlens, positions, counts):
-        lay, Hp, Dp, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-        if (Hp, Dp) != (Hkv, D):
-            raise ValueError(f"the pools hold [{Hp}, {Dp}] a token, k [{Hkv}, {D}]")
-        kp, ks = _strided(k, "k", B, T, Hkv, D, torch.bfloat16)
-        vp, vs = _strided(v, "v", B, T, Hkv, D, torch.bfloat16)
-        fn, name, rope = _rope_arg("atflash_cache_append", rope_base, theta, D)
-        _check(fn(kp, ks, vp, vs, _dev(kpages, "kpages"), _dev(vpages, "vpages"),
-                  _ints(block_table, "block_table", (B, block_table.shape[-1])), _ints(seqlens, "seqlens", (B,)),
-                  _ints(positions, "positions", (B, T)), _ints(counts, "counts", (B,)), B, T, Hkv, block_table.shape[-1],
-                  num_pages, int(page_size), D, rope, int(bool(kcache_rotated)), lay, _stream_ptr(stream)), name)
+    i32, bf16 = torch.int32, torch.bfloat16
+    dev = _device_of(k, v, kpages, vpages, block_table, seqlens, positions, counts)
+    lay, Hp, Dp, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, bf16)
+    if Hp != Hkv or Dp != D:
+        raise ValueError(f"the pools hold [{Hp}, {Dp}] a token, k [{Hkv}, {D}]")
+    kp, ks = _strided(k, "k", (B, T, Hkv, D), bf16)
+    vp, vs = _strided(v, "v", (B, T, Hkv, D), bf16)
+    max_pages = block_table.shape[-1]
+    fn, name, rope = _rope_arg("atflash_cache_append", rope_base, theta, D)
+    _launch(fn, name, dev, stream, (), kp, ks, vp, vs, kpp, vpp, _flat(block_table, "block_table", (B, max_pages), i32),
+            _flat(seqlens, "seqlens", (B,), i32), _flat(positions, "positions", (B, T), i32),
+            _flat(counts, "counts", (B,), i32), B, T, Hkv, max_pages, num_pages, int(page_size), D, rope,
+            int(bool(kcache_rotated)), lay)
 
 
 def tree_decode_workspace_bytes(B, T, Hq, Hkv, D) -> int:
@@ -611,39 +631,36 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
     """
     torch = _torch()
     B, T, Hq, D = q.shape
-    with _same_device(q, kpages, vpages, block_table, seqlens, tree_mask, positions, counts, out, lse, workspace):
-        lay, Hkv, Dp, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-        if Dp != D:
-            raise ValueError(f"the pools hold heads of {Dp} dims, q of {D}")
-        qp, qs = _strided(q, "q", B, T, Hq, D, torch.bfloat16)
-        mask = None
-        if tree_mask is not None:
-            if tree_mask.dtype not in (torch.bool, torch.uint8):
-                raise TypeError("tree_mask must be uint8 or bool")
-            if tuple(tree_mask.shape) != (B, T, T):
-                raise ValueError(f"tree_mask must be [{B}, {T}, {T}], got {tuple(tree_mask.shape)}")
-            mask = _dev(tree_mask, "tree_mask")
-        make = torch.empty if counts is None else torch.zeros
-        fresh = [None, None, None]
-        if out is None:
-            out = fresh[0] = make((B, T, Hq, D), dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
-        elif tuple(out.shape) != (B, T, Hq, D):
-            raise ValueError(f"out must be [{B}, {T}, {Hq}, {D}], got {tuple(out.shape)}")
-        if lse is None and return_lse:
-            lse = fresh[1] = make((B, Hq, T), dtype=torch.float32, device=q.device)
-        elif lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T)):
-            raise ValueError(f"lse must be float32 [{B}, {Hq}, {T}]")
-        need = tree_decode_workspace_bytes(B, T, Hq, Hkv, D)
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = fresh[2] = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        fn, name, rope = _rope_arg("atflash_tree_decode_paged", rope_base, theta, D)
-        sp = _on_stream(stream, *fresh)
-        _check(fn(qp, qs, _dev(kpages, "kpages"), _dev(vpages, "vpages"),
-                  _ints(block_table, "block_table", (B, block_table.shape[-1])), _ints(seqlens, "seqlens", (B,)), mask,
-                  _ints(positions, "positions", (B, T)), _ints(counts, "counts", (B,)), _dev(out, "out"),
-                  _dev(lse, "lse") if lse is not None else None, B, T, Hq, Hkv, block_table.shape[-1], num_pages,
-                  int(page_size), D, rope, float(k_window), lay, _dtype_code(out), _dev(workspace, "workspace"), need,
-                  sp), name)
+    i32, bf16 = torch.int32, torch.bfloat16
+    dev = _device_of(q, kpages, vpages, block_table, seqlens, tree_mask, positions, counts, out, lse, workspace)
+    lay, Hkv, Dp, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, bf16)
+    if Dp != D:
+        raise ValueError(f"the pools hold heads of {Dp} dims, q of {D}")
+    qp, qs = _strided(q, "q", (B, T, Hq, D), bf16)
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.bool and tree_mask.dtype != torch.uint8:
+            raise TypeError("tree_mask must be uint8 or bool")
+        mask = _flat(tree_mask, "tree_mask", (B, T, T), tree_mask.dtype)
+    new_out = new_lse = new_ws = None
+    make = torch.empty if counts is None else torch.zeros
+    if out is None:
+        out = new_out = make((B, T, Hq, D), dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = new_lse = make((B, Hq, T), dtype=torch.float32, device=q.device)
+    need = lib().atflash_tree_decode_workspace_bytes(B, T, Hq, Hkv, D)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = new_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    max_pages = block_table.shape[-1]
+    fn, name, rope = _rope_arg("atflash_tree_decode_paged", rope_base, theta, D)
+    _launch(fn, name, dev, stream, (new_out, new_lse, new_ws), qp, qs, kpp, vpp,
+            _flat(block_table, "block_table", (B, max_pages), i32), _flat(seqlens, "seqlens", (B,), i32), mask,
+            _flat(positions, "positions", (B, T), i32), _flat(counts, "counts", (B,), i32),
+            _flat(out, "out", (B, T, Hq, D), out.dtype), _flat(lse, "lse", (B, Hq, T), torch.float32), B, T, Hq, Hkv,
+            max_pages, num_pages, int(page_size), D, rope, float(k_window), lay, _dtype_code(out),
+            workspace.data_ptr(), need)
     return (out, lse) if lse is not None else out
 
 
@@ -657,17 +674,17 @@ def cache_compact(kpages, vpages, block_table, seqlens, path, accepted, page_siz
     """
     torch = _torch()
     B, M = path.shape
-    with _same_device(kpages, vpages, block_table, seqlens, path, accepted, new_seqlens):
-        lay, Hkv, D, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-        fresh = None
-        if new_seqlens is None:
-            new_seqlens = fresh = torch.empty((B,), dtype=torch.int32, device=seqlens.device)
-        sp = _on_stream(stream, fresh)
-        _check(lib().atflash_cache_compact(
-            _dev(kpages, "kpages"), _dev(vpages, "vpages"), _ints(block_table, "block_table", (B, block_table.shape[-1])),
-            _ints(seqlens, "seqlens", (B,)), _ints(path, "path", (B, M)), _ints(accepted, "accepted", (B,)),
-            _ints(new_seqlens, "new_seqlens", (B,)), B, M, Hkv, block_table.shape[-1], num_pages, int(page_size), D, lay,
-            sp), "atflash_cache_compact")
+    i32 = torch.int32
+    dev = _device_of(kpages, vpages, block_table, seqlens, path, accepted, new_seqlens)
+    lay, Hkv, D, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+    fresh = None
+    if new_seqlens is None:
+        new_seqlens = fresh = torch.empty((B,), dtype=i32, device=seqlens.device)
+    max_pages = block_table.shape[-1]
+    _launch(lib().atflash_cache_compact, "atflash_cache_compact", dev, stream, (fresh,), kpp, vpp,
+            _flat(block_table, "block_table", (B, max_pages), i32), _flat(seqlens, "seqlens", (B,), i32),
+            _flat(path, "path", (B, M), i32), _flat(accepted, "accepted", (B,), i32),
+            _flat(new_seqlens, "new_seqlens", (B,), i32), B, M, Hkv, max_pages, num_pages, int(page_size), D, lay)
     return new_seqlens
 
 
@@ -676,13 +693,12 @@ def cache_copy_pages(kpages, vpages, src, dst, page_size: int, *, tokens=None, k
     V, in place (int32 [n] each).  A page must not be the destination of two copies, nor
     of one and the source of another."""
     torch = _torch()
-    n = src.numel()
-    with _same_device(kpages, vpages, src, dst, tokens):
-        lay, Hkv, D, num_pages = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-        _check(lib().atflash_cache_copy_pages(
-            _dev(kpages, "kpages"), _dev(vpages, "vpages"), _ints(src, "src", (n,)), _ints(dst, "dst", (n,)),
-            _ints(tokens, "tokens", (n,)), n, Hkv, num_pages, int(page_size), D, lay, _stream_ptr(stream)),
-            "atflash_cache_copy_pages")
+    n, i32 = src.numel(), torch.int32
+    dev = _device_of(kpages, vpages, src, dst, tokens)
+    lay, Hkv, D, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
+    _launch(lib().atflash_cache_copy_pages, "atflash_cache_copy_pages", dev, stream, (), kpp, vpp,
+            _flat(src, "src", (n,), i32), _flat(dst, "dst", (n,), i32), _flat(tokens, "tokens", (n,), i32), n, Hkv,
+            num_pages, int(page_size), D, lay)
 
 
 def device_status(clear: bool = True) -> int:

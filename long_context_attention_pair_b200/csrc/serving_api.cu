@@ -14,9 +14,14 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 // Frequencies (at most pi) to turn counts of at most 2^63, in long double so that
 // the quotient adds no error to the table's own.
-RopeTurns turns_of(int dims, const double *theta) {
-    RopeTurns rt;
-    memset(&rt, 0, sizeof(rt));
+const RopeTurns &turns_of(int dims, const double *theta) {
+    static thread_local struct {
+        double theta[kMaxPairs];
+        RopeTurns rt;
+    } last;  // (zero pairs at first)
+    RopeTurns &rt = last.rt;
+    if (rt.pairs == dims / 2 && memcmp(theta, last.theta, sizeof(double) * (dims / 2)) == 0) return rt;
+    memcpy(last.theta, theta, sizeof(double) * (dims / 2));
     rt.pairs = dims / 2;
     for (int r = 0; r < rt.pairs; ++r)
         rt.turn[r] = (uint64_t)rintl((long double)theta[r] / 6.283185307179586476925286766559L * 18446744073709551616.0L);
@@ -47,10 +52,24 @@ int check_table(int B, int max_pages, int page_size) {
     return ATFLASH_OK;
 }
 
+// The frequency table of a base, and turn counts of a table: a serving loop asks for the
+// same ones at every call, so each thread keeps the last (compared by value).
 struct BaseTheta {
-    double theta[kMaxPairs];
+    const double *theta = nullptr;
     int rc;
-    BaseTheta(int D, double base) : rc(theta_from_base(D, base, theta)) {}
+    BaseTheta(int D, double base) {
+        static thread_local struct {
+            int D = 0;
+            double base = 0, theta[kMaxPairs];
+        } last;
+        if (last.D != D || last.base != base) {
+            last.D = 0;
+            if ((rc = theta_from_base(D, base, last.theta)) != ATFLASH_OK) return;
+            last.D = D, last.base = base;
+        }
+        rc = ATFLASH_OK;
+        theta = last.theta;
+    }
 };
 
 int done(cudaError_t e) { return e == cudaSuccess ? ATFLASH_OK : ATFLASH_ERR_CUDA; }

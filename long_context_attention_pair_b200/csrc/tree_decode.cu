@@ -48,6 +48,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "ptx.cuh"
 #include "serving.h"
 
@@ -1254,13 +1256,20 @@ cudaError_t launch(const TreeArgs &a, const WindowParams &wp, const RopeTurns &r
         e = make_map(&tk, a.kpages, 4, dv, sv, bv, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (e != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(tree_decode_kernel<D, kPacked, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Request)) !=
-        cudaSuccess)
-        return e;
-    // The in-kernel register split assumes this launch count: refuse to run otherwise.
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, tree_decode_kernel<D, kPacked, NC>)) != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    // Once per device: the shared memory, and that the in-kernel register split finds the
+    // launch count it assumes.
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        const auto kernel = tree_decode_kernel<D, kPacked, NC>;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Request)) != cudaSuccess) return e;
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
     tree_decode_kernel<D, kPacked, NC><<<sh.groups * sh.R, kThreads, Cfg<D>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.T * a.Hq;

@@ -115,4 +115,14 @@ def test_python_checks_come_before_the_library():
         atf._pools(pool, pool, 64, "PACKED", torch.bfloat16)
     with pytest.raises(TypeError, match="bfloat16"):
         atf._pools(pool.float(), pool, 64, "NHD", torch.bfloat16)
-    assert atf._pools(pool, pool, 64, "NHD", torch.bfloat16) == (atf.KV_NHD, 2, 64, 3)
+    assert atf._pools(pool, pool, 64, "NHD", torch.bfloat16)[:4] == (atf.KV_NHD, 2, 64, 3)
+    with pytest.raises(TypeError, match="int32"):
+        atf._flat(pos.long(), "positions", (1, 2), torch.int32)
+    with pytest.raises(ValueError, match="positions"):
+        atf._flat(pos, "positions", (2, 1), torch.int32)
+    with pytest.raises(ValueError, match="contiguous"):
+        atf._flat(torch.zeros(2, 4, dtype=torch.int32).T, "path", (4, 2), torch.int32)
+    with pytest.raises(ValueError, match="last dimension"):
+        atf._strided(torch.zeros(1, 2, 64, 4).transpose(2, 3), "q", (1, 2, 4, 64), torch.float32)
+    with pytest.raises(ValueError, match="expanded"):
+        atf._strided(torch.zeros(1, 1, 4, 64).expand(1, 2, 4, 64), "out_q", (1, 2, 4, 64), torch.float32, True)
