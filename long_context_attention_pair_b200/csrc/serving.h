@@ -31,11 +31,31 @@ __device__ __forceinline__ float2 turn_cos_sin(int32_t pos, uint64_t turn) {
     return make_float2(c, s);
 }
 
+// The same by the hardware's sin and cos, within 2^-21 on [-pi, pi]: for results rounded
+// to bf16 (2^-8 of their value).
+__device__ __forceinline__ float2 turn_cos_sin_fast(int32_t pos, uint64_t turn) {
+    float s, c;
+    __sincosf((float)(int64_t)((uint64_t)(int64_t)pos * turn) * 3.4061215800865545e-19f, &s, &c);  // 2 pi / 2^64
+    return make_float2(c, s);
+}
+
+// 16 bytes copied to shared memory asynchronously; groups of copies are waited for in order.
+__device__ __forceinline__ void copy_async(void *smem, const void *global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the latest N groups have landed
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Pool page of a cache slot; -1, recorded in the device status word, for a slot
 // outside the sequence's table row or a page id outside the pool.
 __device__ __forceinline__ int page_of(const PagedKV &pk, int b, int64_t slot, int *status) {
-    const int64_t i = slot / pk.page_size;
-    int page = (slot >= 0 && i < pk.max_pages) ? pk.block_table[(size_t)b * pk.max_pages + i] : -1;
+    // (A slot that the row has room for fits 31 bits: no 64-bit division.)
+    const bool inside = slot >= 0 && slot < (int64_t)pk.max_pages * pk.page_size;
+    const uint32_t i = inside ? (uint32_t)slot / (uint32_t)pk.page_size : 0u;
+    int page = inside ? pk.block_table[(size_t)b * pk.max_pages + i] : -1;
     if (page < 0 || page >= pk.num_pages) {
         atomicCAS(status, 0, ATFLASH_DEVICE_BAD_PAGE);
         page = -1;

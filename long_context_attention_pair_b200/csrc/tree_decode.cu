@@ -808,9 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t wa = i < 2 ? ya.x : ya.y, wb = i < 2 ? yb.x : yb.y;
                         const float fa = i & 1 ? bf16hi(wa) : bf16lo(wa), fb = i & 1 ? bf16hi(wb) : bf16lo(wb);
                         // The hardware's sin and cos (2^-21 on [-pi, pi]) lie far below the 2^-16 of hi + lo.
-                        float sn, cs;
-                        __sincosf((float)(int64_t)((uint64_t)(int64_t)pos * turn[i]) * 3.4061215800865545e-19f, &sn, &cs);
-                        const float x = fa * cs - fb * sn, y = fb * cs + fa * sn;
+                        const float2 cs = turn_cos_sin_fast(pos, turn[i]);
+                        const float x = fa * cs.x - fb * cs.y, y = fb * cs.x + fa * cs.y;
                         hi[i] = pack_bf16x2(x, y);
                         lo[i] = pack_bf16x2(x - bf16lo(hi[i]), y - bf16hi(hi[i]));
                     }
