@@ -107,7 +107,7 @@ struct Segment {
 struct Ctl {
     uint64_t seg_full[kRing], seg_empty[kRing];
     uint64_t q_ready;
-    uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
+    uint64_t k_full[4], k_ready[4], k_empty[4], v_full[4], v_tail[4], v_ready[4], v_empty[4];
     uint64_t s_full[kBufs], p_full[kBufs], o_done[kBufs];  // per S / P buffer
     uint64_t m_full[2], m_empty[2];
     uint64_t max_bar[2][4];          // per set and lane quarter: the running max after its tile is posted
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&ctl->k_ready[s], 1);
                 mbar_init(&ctl->k_empty[s], 1 + 4);
                 mbar_init(&ctl->v_full[s], 1);
+                mbar_init(&ctl->v_tail[s], 1);
                 mbar_init(&ctl->v_ready[s], 2);
                 mbar_init(&ctl->v_empty[s], 1);
             }
@@ -506,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 const int ca = v || !kPacked ? 0 : r_lo >> 3;
                 if (lane == 0) {
+                    if (v && m0 + kBN > g.L) mbar_arrive(&ctl->v_tail[st]);  // a tile with nodes is on its way
                     if (!v) ctl->band[it % 8] = make_band<kPacked>(r_lo, r_full, g.pmin != g.pmax);
                     mbar_expect_tx(&full[st], (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves);
                 }
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kTail) {
         // ---------------- tiles with nodes: mask bits, V behind the last node
         const int t2 = warp - kTail;
-        uint32_t used = 0;  // phase bit of each set's mask buffer
+        uint32_t used = 0, tails = 0;  // phase bits of each set's mask buffer, of v_tail per stage
         while (ok && runs.next(wc, ok)) {
             const Segment g = runs.now();
             runs.done(lane);
@@ -644,6 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V behind the last node may hold anything (0 * NaN must not reach O), and so may
                 // a node that some rows do not see: its non-finite values are taken out here and
                 // put back, for the rows that see them, at the end of the run.
+                // These warps skip the tiles before, so they may look at v_full only once its phase can
+                // be this tile's: the V producer says when.
+                if (!(ok = wait(&ctl->v_tail[st], (tails >> st) & 1, wc, 66))) break;
+                tails ^= 1u << st;
                 if (!(ok = wait(&ctl->v_full[st], (it / ST) & 1, wc, 45))) break;
                 uint8_t *vst = sV + st * F::TileBytes;
                 constexpr int kUnits = D / 8;  // 16-byte units of a row

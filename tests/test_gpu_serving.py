@@ -246,6 +246,39 @@ def test_tree_long_and_ragged(packed):
 
 
 @pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv,page,lens,T,k", [
+    (128, 7, 1, 128, [200033], 1, math.inf),      # ten key tiles per SM, one row group, copies of the rows
+    (64, 20, 2, 64, [120001, 3, 40007], 2, 8.0),
+    (128, 6, 2, 64, [100100, 517], 9, 16.0),      # 27 rows
+    (64, 9, 1, 256, [250001], 6, 2.0),            # 54 rows: two copies
+    (128, 14, 2, 256, [90000, 60001], 21, 16.0),  # 147 rows: two row tiles
+])
+def test_tree_many_tiles_in_a_row(packed, D, Hq, Hkv, page, lens, T, k):
+    # Long runs of key tiles on every SM, with tiles of nodes after them: every pipeline wraps many times.
+    run_tree(D, Hq, Hkv, page, packed, lens, T, None, "tree", k, base=1e6, seed=311)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_tree_every_key_counts_once(packed):
+    # Uniform weights (queries of zeros) over one-hot values by key tile: output dim d is the share of the keys
+    # in tiles d mod D, which one lost or doubled run of keys would change.
+    B, T, Hq, Hkv, D, page, L = 3, 3, 6, 2, 64, 128, 70017
+    c = R.Cache(B, (L + T + page - 1) // page, page, Hkv, D, packed, 321)
+    slots = torch.arange(L + T, device="cuda")
+    v = torch.nn.functional.one_hot(slots // 128 % D, D).to(torch.bfloat16)[:, None].expand(-1, Hkv, -1).contiguous()
+    for b in range(B):
+        c.write(b, slots, randn((L + T, Hkv, D), 322 + b), v)
+    out, lse = atf.tree_decode_paged(torch.zeros((B, T, Hq, D), dtype=torch.bfloat16, device="cuda"), c.kpages, c.vpages, c.block_table,
+                                     ints([L] * B), page, 1e4, 8.0, kv_layout=c.layout, return_lse=True, out_dtype=torch.float32)
+    for i in range(T):
+        n = L + i + 1
+        want = torch.bincount(slots[:n] // 128 % D, minlength=D).double() / n
+        # Powers of two times counts: every product and sum is exact in fp32, one division at the end.
+        assert float(((out[:, i].double() - want).abs() / want).max()) <= 2.0 ** -22
+        assert float((lse[:, :, i].double() - math.log(n)).abs().max()) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("packed", [False, True])
 def test_tree_scaled_frequencies(packed):
     import scaled
     D, Hq, Hkv, page, T, L = 128, 8, 2, 64, 6, 400
