@@ -68,6 +68,7 @@ static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "reg
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
 constexpr int kStaged = 16;      // boundary pairs staged per tile (at least one natural K-step)
+constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences)
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -150,7 +151,10 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, const Shape &sh, int b)
     s.groups = (int)(((uint32_t)s.nodes * (uint32_t)sh.G + (uint32_t)(kBM * sh.R) - 1u) / (uint32_t)(kBM * sh.R));  // B*T*Hq < 2^31
     return s;
 }
-__device__ __forceinline__ int64_t units_of(const Seq &s, int Hkv) { return (int64_t)Hkv * s.groups * s.tiles; }
+// Units of one item, and of a sequence: its tiles and kItemCost for what a run costs beside
+// them (queries in, state out, the boundary pairs near the queries), counted at its end.
+__device__ __forceinline__ int item_units(const Seq &s) { return s.tiles ? s.tiles + kItemCost : 0; }
+__device__ __forceinline__ int64_t units_of(const Seq &s, int Hkv) { return (int64_t)Hkv * s.groups * item_units(s); }
 
 // Units before sequence `b` (all of them for b = B), by a whole warp.
 __device__ __forceinline__ int64_t units_before(const TreeArgs &a, const Shape &sh, int b) {
@@ -435,7 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s = seq_of(a, sh, ++b);
                     continue;
                 }
-                const int item = (int)(off >> 31 ? off / s.tiles : (uint32_t)off / (uint32_t)s.tiles);
+                const int per = item_units(s);
+                const int item = (int)(off >> 31 ? off / per : (uint32_t)off / (uint32_t)per);
+                const int v0 = (int)(off - (int64_t)item * per), nv = (int)min((int64_t)(per - v0), left);
+                off += nv;
+                left -= nv;
                 g.b = b;
                 g.h = item / s.groups;
                 g.L = (int)s.L;
@@ -443,10 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.row0 = (item % s.groups * sh.R + member) * kBM;
                 g.rows = min(kBM, s.nodes * sh.G - g.row0);
                 g.tiles = s.tiles;
-                g.tile0 = (int)(off - (int64_t)item * s.tiles);
-                g.ntile = (int)min((int64_t)(s.tiles - g.tile0), left);
-                off += g.ntile;
-                left -= g.ntile;
+                g.tile0 = min(v0, s.tiles);
+                g.ntile = min(v0 + nv, s.tiles) - g.tile0;
+                if (g.ntile == 0) g.rows = 0;  // nothing but the item's cost
                 if (g.rows > 0) break;
                 g.rows = 0;  // this CTA's row tile does not exist in this item
             }
@@ -1182,7 +1189,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     pdl_wait();  // by every warp, so that this grid never ends before the one it depends on
     if (!exists || i >= s.nodes) return;
     const int h = hq / sh.G, r = i * sh.G + hq % sh.G, rt = r / kBM;
-    const int64_t first = before + ((int64_t)h * s.groups + rt / sh.R) * s.tiles;
+    const int64_t first = before + ((int64_t)h * s.groups + rt / sh.R) * item_units(s);
     const int active = active_groups(total, sh.groups);
     // Group of unit x: the largest g with floor(g * total / active) <= x.
     const auto group_of = [&](int64_t x) {
