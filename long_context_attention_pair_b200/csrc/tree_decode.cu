@@ -67,13 +67,12 @@ constexpr int kLaunchRegs = 128, kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
-constexpr int kStaged = 16;      // boundary pairs staged per tile (at least one natural K-step)
 constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences)
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-template <int D>
+template <int D, bool kPacked>
 struct Cfg {
     static constexpr int H = D / 2;
     static constexpr int C = D / 16;                 // K-steps
@@ -82,10 +81,14 @@ struct Cfg {
     static constexpr int OffQ = 0;                   // also the fp32 exchange of repeated rows: 128 x D x 4
     static constexpr int OffK = OffQ + 2 * TileBytes;
     static constexpr int OffV = OffK + ST * TileBytes;
-    static constexpr int OffStage = OffV + ST * TileBytes;       // [ST][kStaged][128] words (k_r, k_{r+H})
-    static constexpr int StageBytes = kStaged * kBN * 4;
-    static constexpr int OffKpos = OffStage + ST * StageBytes;   // [ST][128] key positions
-    static constexpr int OffMask = OffKpos + ST * kBN * 4;       // [2][128] rows of 128 mask bits, one per node
+    // Boundary pairs staged per tile (at least those of one K-step), and buffers of them.  A
+    // packed tile's K stage is released when its QK is done, so its staged pairs need a ring
+    // that is rewritten only after its softmax: K of tile it + Cells is loaded after QK(it + 3),
+    // which waits for PV(it).  In natural order the softmax holds the K stage instead.
+    static constexpr int Staged = kPacked ? 8 : 16, Cells = kPacked ? ST + 3 : ST;
+    static constexpr int OffStage = OffV + ST * TileBytes;       // [Cells][Staged][128] words (k_r, k_{r+H})
+    static constexpr int OffKpos = OffStage + Cells * Staged * kBN * 4;  // [Cells][128] key positions
+    static constexpr int OffMask = OffKpos + Cells * kBN * 4;    // [2][128] rows of 128 mask bits, one per node
     static constexpr int OffCtl = OffMask + 2 * kBM * 16;
     static constexpr int CtlBytes = 6144;
     static constexpr int Request = OffCtl + CtlBytes + 1024;
@@ -118,8 +121,8 @@ struct Ctl {
     Segment seg[kRing];
     int4 band[8];                    // of tile it in entry it % 8: (r_lo, rs, r_full, flags), see make_band.  (A tile's
                                      // entry is rewritten only after its PV, hence after every reader.)
-    uint32_t chunks[4];              // 32-key chunks of the tile in which cells are added
-    uint32_t zone[4][kStaged];       // of staged pair rs + i: first key and end of the keys added per cell
+    uint32_t chunks[7];              // 32-key chunks of the tile in which cells are added
+    uint32_t zone[7][16];            // of staged pair rs + i: first key and end of the keys added per cell
     int nf_seg[8];                   // run (mod 8) whose tree holds a non-finite value
     int w[64];
     uint64_t turn[64];
@@ -215,12 +218,15 @@ constexpr int kPairsPerStep = kPacked ? 8 : 16;
 // cell for every key, straight from the K tile (only when more pairs are boundary
 // than can be staged); [rs, r_full) staged, the MMA keeping the keys that every row
 // keeps; r >= r_full kept for every cell.  The MMA starts at the K-step of rs.
-enum : int { kBandFix = 1, kBandCells = 2 };  // the fix-up warp has work; some cells are added
-template <bool kPacked>
+// Flags: boundary pairs exist (the fix-up warp has work); some cells are added; the
+// softmax warps hold the K stage.
+enum : int { kBandFix = 1, kBandCells = 2, kBandHold = 4 };
+template <int D, bool kPacked>
 __device__ __forceinline__ int4 make_band(int r_lo, int r_full, bool spread) {
-    constexpr int kPer = kPairsPerStep<kPacked>;
+    constexpr int kPer = kPairsPerStep<kPacked>, kStaged = Cfg<D, kPacked>::Staged;
     const int rs = r_full - r_lo > kStaged ? (r_full - kStaged + kPer - 1) / kPer * kPer : r_lo;
-    const int flags = (r_lo < r_full || rs % kPer != 0 ? kBandFix : 0) | (r_lo < rs || (spread && r_lo < r_full) ? kBandCells : 0);
+    int flags = r_lo < r_full ? kBandFix : 0;
+    if (r_lo < rs || (spread && r_lo < r_full)) flags |= kBandCells | (!kPacked || r_lo < rs ? kBandHold : 0);
     return make_int4(r_lo, rs, r_full, flags);
 }
 
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ TreeArgs a, const __grid_constant__ Shape sh,
                        const __grid_constant__ WindowParams wp, const __grid_constant__ RopeTurns rt, int box_keys) {
-    using F = Cfg<D>;
+    using F = Cfg<D, kPacked>;
+    constexpr int kStaged = F::Staged;
     constexpr int H = F::H, C = F::C, ST = F::ST;
     constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
     constexpr int kPer = kPairsPerStep<kPacked>;
@@ -511,20 +518,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r_lo = prefix ? first_kept(w0, w1, g.pmin - (m0 + kBN - 1)) : 0;
                     r_full = first_kept(w0, w1, g.pmax - (prefix || (m0 < g.L && m0 < g.kmin) ? m0 : (int64_t)g.kmin));
                 }
-                if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 const int ca = v || !kPacked ? 0 : r_lo >> 3;
+                const uint32_t bytes = (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves;
+                uint8_t *dst = (v ? sV : sK) + st * F::TileBytes + (kPacked && !v ? u * 4096 + hf * 2048 : u * 16384 + hf * 8192);
+                const bool mine = issue && (kPacked && !v ? u >= ca && u < C : u < D / 64);
+                const int z = (pg * sh.Hkv + g.h) * C + u;
+                if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 if (lane == 0) {
                     if (v && m0 + kBN > g.L) mbar_arrive(&ctl->v_tail[st]);  // a tile with nodes is on its way
-                    if (!v) ctl->band[it % 8] = make_band<kPacked>(r_lo, r_full, g.pmin != g.pmax);
-                    mbar_expect_tx(&full[st], (v || !kPacked ? (uint32_t)(D / 64) * 8192u : (uint32_t)(C - ca) * 2048u) * halves);
+                    if (!v) ctl->band[it % 8] = make_band<D, kPacked>(r_lo, r_full, g.pmin != g.pmax);
+                    mbar_expect_tx(&full[st], bytes);
                 }
                 __syncwarp();
-                uint8_t *dst = (v ? sV : sK) + st * F::TileBytes;
-                if (kPacked && !v) {
-                    if (issue && u >= ca && u < C)
-                        tma_load_3d(dst + u * 4096 + hf * 2048, &tm_k, &full[st], 0, at, (pg * sh.Hkv + g.h) * C + u);
-                } else if (issue && u < D / 64) {
-                    tma_load_4d(dst + u * 16384 + hf * 8192, v ? &tm_v : &tm_k, &full[st], 64 * u, g.h, at, pg);
+                if (mine) {
+                    if (kPacked && !v) tma_load_3d(dst, &tm_k, &full[st], 0, at, z);
+                    else tma_load_4d(dst, v ? &tm_v : &tm_k, &full[st], 64 * u, g.h, at, pg);
                 }
             }
         }
@@ -540,78 +548,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             runs.done(lane);
             const int64_t end = (int64_t)g.L + g.nodes;
             for (int j = g.tile0; ok && j < g.tile0 + g.ntile; ++j, ++it) {
-                const int st = it % ST;
+                const int st = it % ST, cb = it % F::Cells;
                 const int64_t m0 = (int64_t)j * kBN;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
                 const int4 bd = ctl->band[it % 8];
                 if (!(bd.w & kBandFix)) continue;
                 uint8_t *kst = sK + st * F::TileBytes;
                 constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
-                // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
-                const int z = bd.y % kPer;
-                if (z) {
-                    const int c = bd.y / kPer;
+                const bool prefix = m0 + kBN <= g.L;
+                int kp[kK];
 #pragma unroll
-                    for (int e = 0; e < kK; ++e) {
-                        if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + 32 * e, 0), kst + c * 4096 + sw32_off(lane + 32 * e, 4), z);
-                        else {
-                            for (int half = 0; half < 2; ++half) {
-                                const int d = 16 * c + half * H;
-                                uint8_t *u0 = kst + sw128_off(lane + 32 * e, d), *u1 = kst + sw128_off(lane + 32 * e, d + 8);
-                                zero_words(u0, u1, z / 2);
-                                if (z & 1) *reinterpret_cast<uint16_t *>((z < 8 ? u0 : u1) + (z & 6) * 2) = 0;
-                            }
-                        }
-                    }
+                for (int e = 0; e < kK; ++e) {
+                    const int64_t slot = m0 + lane + 32 * e;
+                    kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
+                    if (bd.w & kBandCells) sKpos[cb * kBN + lane + 32 * e] = kp[e];
                 }
-                if (bd.x < bd.z) {
-                    const bool prefix = m0 + kBN <= g.L;
-                    int kp[kK];
+                uint32_t chunks = prefix ? 0u : 0xfu;  // 32-key chunks in which some cell is added
+                // Addresses of this lane's first key; its others are 32 rows further each.
+                const uint8_t *row0 = kst + (kPacked ? lane * 32 : lane * 128);
+                const uint32_t swz = kPacked ? (lane & 4) << 2 : (lane & 7) << 4;
+                for (int r = bd.y; r < bd.z; ++r) {
+                    // Keys at positions >= all are kept by every row, below none by no row.
+                    const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
+                    uint32_t *stage = sStage + (cb * kStaged + r - bd.y) * kBN + lane;
+                    uint8_t *x0, *x1 = nullptr;
+                    if (kPacked) {
+                        x0 = const_cast<uint8_t *>(row0) + (r >> 3) * 4096 + (((r & 7) * 4) ^ swz);
+                    } else {
+                        x0 = const_cast<uint8_t *>(row0) + (r >> 6) * 16384 + ((((r & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                        x1 = const_cast<uint8_t *>(row0) + ((r + H) >> 6) * 16384 + (((((r + H) & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
+                    }
 #pragma unroll
                     for (int e = 0; e < kK; ++e) {
-                        const int64_t slot = m0 + lane + 32 * e;
-                        kp[e] = slot < g.L || slot >= end ? (int)slot : node_pos(a, g.b, g.L, (int)(slot - g.L));
-                        if (bd.w & kBandCells) sKpos[st * kBN + lane + 32 * e] = kp[e];
-                    }
-                    uint32_t chunks = prefix ? 0u : 0xfu;  // 32-key chunks in which some cell is added
-                    // Addresses of this lane's first key; its others are 32 rows further each.
-                    const uint8_t *row0 = kst + (kPacked ? lane * 32 : lane * 128);
-                    const uint32_t swz = kPacked ? (lane & 4) << 2 : (lane & 7) << 4;
-                    for (int r = bd.y; r < bd.z; ++r) {
-                        // Keys at positions >= all are kept by every row, below none by no row.
-                        const int64_t all = (int64_t)g.pmax - w[r], none = (int64_t)g.pmin - w[r];
-                        uint32_t *stage = sStage + (st * kStaged + r - bd.y) * kBN + lane;
-                        uint8_t *x0, *x1 = nullptr;
+                        if (kp[e] >= all) continue;
                         if (kPacked) {
-                            x0 = const_cast<uint8_t *>(row0) + (r >> 3) * 4096 + (((r & 7) * 4) ^ swz);
+                            uint32_t *x = reinterpret_cast<uint32_t *>(x0 + e * 1024);
+                            if (kp[e] >= none) stage[32 * e] = *x;
+                            *x = 0;
                         } else {
-                            x0 = const_cast<uint8_t *>(row0) + (r >> 6) * 16384 + ((((r & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
-                            x1 = const_cast<uint8_t *>(row0) + ((r + H) >> 6) * 16384 + (((((r + H) & 63) >> 3) << 4) ^ swz) + (r & 7) * 2;
-                        }
-#pragma unroll
-                        for (int e = 0; e < kK; ++e) {
-                            if (kp[e] >= all) continue;
-                            if (kPacked) {
-                                uint32_t *x = reinterpret_cast<uint32_t *>(x0 + e * 1024);
-                                if (kp[e] >= none) stage[32 * e] = *x;
-                                *x = 0;
-                            } else {
-                                uint16_t *lo = reinterpret_cast<uint16_t *>(x0 + e * 4096), *hi = reinterpret_cast<uint16_t *>(x1 + e * 4096);
-                                if (kp[e] >= none) stage[32 * e] = *lo | (uint32_t)*hi << 16;
-                                *lo = 0;
-                                *hi = 0;
-                            }
-                        }
-                        if (none < all) {
-                            // Staged keys lie in [z0, z1) of a prefix tile, anywhere in one with nodes.
-                            const int z0 = prefix ? (int)min(max(none - m0, (int64_t)0), (int64_t)kBN) : 0;
-                            const int z1 = prefix ? (int)min(max(all - m0, (int64_t)0), (int64_t)kBN) : kBN;
-                            if (lane == 0) ctl->zone[st][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
-                            if (z0 < z1) chunks |= (2u << (z1 - 1) / 32) - (1u << z0 / 32);
+                            uint16_t *lo = reinterpret_cast<uint16_t *>(x0 + e * 4096), *hi = reinterpret_cast<uint16_t *>(x1 + e * 4096);
+                            if (kp[e] >= none) stage[32 * e] = *lo | (uint32_t)*hi << 16;
+                            *lo = 0;
+                            *hi = 0;
                         }
                     }
-                    if (lane == 0) ctl->chunks[st] = bd.x < bd.y ? 0xfu : chunks;
+                    if (none < all) {
+                        // Staged keys lie in [z0, z1) of a prefix tile, anywhere in one with nodes.
+                        const int z0 = prefix ? (int)min(max(none - m0, (int64_t)0), (int64_t)kBN) : 0;
+                        const int z1 = prefix ? (int)min(max(all - m0, (int64_t)0), (int64_t)kBN) : kBN;
+                        if (lane == 0) ctl->zone[cb][r - bd.y] = (uint32_t)z0 | (uint32_t)z1 << 16;
+                        if (z0 < z1) chunks |= (2u << (z1 - 1) / 32) - (1u << z0 / 32);
+                    }
                 }
+                if (lane == 0) ctl->chunks[cb] = bd.x < bd.y ? 0xfu : chunks;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
@@ -699,6 +688,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = it % ST, buf = it % kBufs;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
                 const int4 bd = ctl->band[it % 8];
+                // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
+                const int z = bd.y % kPer;
+                if (z) {
+                    uint8_t *kst = sK + st * F::TileBytes;
+                    const int c = bd.y / kPer;
+#pragma unroll
+                    for (int e = 0; e < kBN; e += 32) {
+                        if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + e, 0), kst + c * 4096 + sw32_off(lane + e, 4), z);
+                        else {
+                            for (int half = 0; half < 2; ++half) {
+                                const int d = 16 * c + half * H;
+                                uint8_t *u0 = kst + sw128_off(lane + e, d), *u1 = kst + sw128_off(lane + e, d + 8);
+                                zero_words(u0, u1, z / 2);
+                                if (z & 1) *reinterpret_cast<uint16_t *>((z < 8 ? u0 : u1) + (z & 6) * 2) = 0;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
                 if (bd.w & kBandFix) {
                     if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
                     fixed ^= 1u << st;
@@ -728,9 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(&ctl->s_full[buf]);
                     umma_commit(&ctl->k_empty[st]);
                     mbar_arrive(&ctl->s_full[buf]);
-                    // The softmax warps read the stage only where cells are added; otherwise their
-                    // arrivals are made here.
-                    if (!(bd.w & kBandCells)) mbar_arrive_n(&ctl->k_empty[st], 4);
+                    // Where the softmax warps do not read the stage, their arrivals are made here.
+                    if (!(bd.w & kBandHold)) mbar_arrive_n(&ctl->k_empty[st], 4);
                 }
                 __syncwarp();
             }
@@ -774,7 +782,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const uint32_t tO = tmem + F::TmemO + lane_off;
         const float scale_log2 = 1.4426950408889634f * rsqrtf((float)D);
-        uint32_t fixed = 0;                              // phase bit of k_ready per stage
         int syncs = 0, tails = 0;
         // All softmax warps (bounded, unlike a named barrier).
         auto soft_sync = [&]() -> bool {
@@ -843,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pmax = g.pmax;
             const int j0 = tile0 + ((it ^ set) & 1);  // this set's tiles
             for (int j = j0; j < tile0 + ntile; j += 2) {
-                const int x = it + (j - tile0), st = x % ST, buf = x % kBufs;
+                const int x = it + (j - tile0), st = x % ST, buf = x % kBufs, cb = x % F::Cells;
                 const uint32_t tS = tmem + buf * kBN + lane_off;  // S, and P over it
                 const bool tail = (int64_t)(j + 1) * kBN > L;
                 if (!(ok = wait(&ctl->s_full[buf], (x / kBufs) & 1, wc, 56))) break;
@@ -851,19 +858,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int4 bd = ctl->band[x % 8];
                 const bool cells = bd.w & kBandCells;
                 bool dense = bd.y < H;  // S holds something
-                if (bd.w & kBandFix) {
-                    // Waited for only where this warp still holds the stage, so that the barrier
-                    // cannot be a phase ahead of it.
-                    if (cells && !(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 57))) break;
-                    fixed ^= 1u << st;
-                }
                 if (tail) {
                     if (!(ok = wait(&ctl->m_full[set], tails & 1, wc, 58))) break;
                     ++tails;
                 }
                 if (cells || tail) {
                     // Cells added or hidden, in S itself, 32 columns at a time.
-                    const uint32_t chunks = (cells ? ctl->chunks[st] : 0u) | (tail || !dense ? 0xfu : 0u);
+                    const uint32_t chunks = (cells ? ctl->chunks[cb] : 0u) | (tail || !dense ? 0xfu : 0u);
 #pragma unroll 1
                     for (int cc = c0; live && cc < c0 + NC; cc += 32) {
                         if (!((chunks >> (cc / 32)) & 1u)) continue;
@@ -880,11 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i) s[i] = 0.f;
                         }
                         if (cells) {
-                            const int4 *kp = reinterpret_cast<const int4 *>(sKpos + st * kBN + cc);
+                            const int4 *kp = reinterpret_cast<const int4 *>(sKpos + cb * kBN + cc);
 #pragma unroll 1
                             for (int r = bd.x; r < bd.z; ++r) {
                                 if (r >= bd.y && !tail) {
-                                    const uint32_t z = ctl->zone[st][r - bd.y];
+                                    const uint32_t z = ctl->zone[cb][r - bd.y];
                                     if ((int)(z >> 16) <= cc || (int)(z & 0xffff) >= cc + 32) continue;
                                 }
                                 const uint32_t qh = load_pair<D, kPacked>(sQ, copy * kRows + row, r);
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const int lim = pos - w[r];
                                 if (r >= bd.y) {
                                     const uint32_t span = (uint32_t)(pmax - pos);
-                                    const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + (st * kStaged + r - bd.y) * kBN + cc);
+                                    const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + (cb * kStaged + r - bd.y) * kBN + cc);
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) {
                                         const uint4 k = kw[i];
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                     for (int i = 0; i < 32; ++i) {
                                         const uint32_t k = load_pair<D, kPacked>(kst, cc + i, r);
-                                        s[i] += sKpos[st * kBN + cc + i] >= lim ? fmaf(qa, bf16lo(k), qb * bf16hi(k)) : 0.f;
+                                        s[i] += sKpos[cb * kBN + cc + i] >= lim ? fmaf(qa, bf16lo(k), qb * bf16hi(k)) : 0.f;
                                     }
                                 }
                             }
@@ -929,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     dense = true;
                     __syncwarp();
-                    if (cells && lane == 0) mbar_arrive(&ctl->k_empty[st]);
+                    if ((bd.w & kBandHold) && lane == 0) mbar_arrive(&ctl->k_empty[st]);
                     if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
                 }
                 // The row's maximum, then the exponentials, CW columns at a time.  Whole rows (NC = 128)
@@ -1276,13 +1277,13 @@ cudaError_t launch(const TreeArgs &a, const WindowParams &wp, const RopeTurns &r
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (!(configured.load(std::memory_order_relaxed) & bit)) {
         const auto kernel = tree_decode_kernel<D, kPacked, NC>;
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Request)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kPacked>::Request)) != cudaSuccess) return e;
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    tree_decode_kernel<D, kPacked, NC><<<sh.groups * sh.R, kThreads, Cfg<D>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
+    tree_decode_kernel<D, kPacked, NC><<<sh.groups * sh.R, kThreads, Cfg<D, kPacked>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.T * a.Hq;
     return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, sh);
