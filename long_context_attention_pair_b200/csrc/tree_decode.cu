@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int H = F::H, C = F::C, ST = F::ST;
     constexpr int kRep = kBN / NC, kRows = kBM / kRep;  // copies of the rows, rows of a copy
     constexpr int kPer = kPairsPerStep<kPacked>;
-    constexpr int CW = NC < 32 ? NC : 32;              // columns in registers at a time
+    constexpr int CW = 32;                             // columns in registers at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem + F::OffQ, *sK = smem + F::OffK, *sV = smem + F::OffV;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < ST; ++s) {
                 mbar_init(&ctl->k_full[s], 1);
                 mbar_init(&ctl->k_ready[s], 1);
-                mbar_init(&ctl->k_empty[s], 1 + 4);
+                mbar_init(&ctl->k_empty[s], 1 + 1 + 4);  // QK, the fix-up warp, the set's softmax warps
                 mbar_init(&ctl->v_full[s], 1);
                 mbar_init(&ctl->v_tail[s], 1);
                 mbar_init(&ctl->v_ready[s], 2);
@@ -552,7 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t m0 = (int64_t)j * kBN;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
                 const int4 bd = ctl->band[it % 8];
-                if (!(bd.w & kBandFix)) continue;
+                __syncwarp();
+                if (!(bd.w & kBandFix)) {
+                    // Seen: without this, the stage could be reloaded before this warp looks at it.
+                    if (lane == 0) mbar_arrive(&ctl->k_empty[st]);
+                    continue;
+                }
                 uint8_t *kst = sK + st * F::TileBytes;
                 constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
                 const bool prefix = m0 + kBN <= g.L;
@@ -603,7 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ctl->chunks[cb] = bd.x < bd.y ? 0xfu : chunks;
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
+                if (lane == 0) {
+                    mbar_arrive(&ctl->k_ready[st]);
+                    mbar_arrive(&ctl->k_empty[st]);
+                }
             }
         }
     } else if (warp >= kTail) {
@@ -933,14 +941,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if ((bd.w & kBandHold) && lane == 0) mbar_arrive(&ctl->k_empty[st]);
                     if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
                 }
-                // The row's maximum, then the exponentials, CW columns at a time.  Whole rows (NC = 128)
-                // are read twice, by loops: their unrolled code would not stay in the instruction cache.
+                // The row's maximum, then the exponentials, CW columns at a time.  More columns are read
+                // twice, by loops: their unrolled code would not stay in the instruction cache (on 8
+                // sequences of 512 nodes: 128 columns unrolled 498 us, 64 at a time 439, 32 384; 16 354 to 32's 343 later).
                 float s[CW], row_max = -INFINITY;
                 auto load = [&](int c) {
                     if (dense) {
                         uint32_t ra[CW];
-                        if constexpr (CW == 64) tmem_ld_32x32b_x64(tS + c, ra);
-                        else tmem_ld_32x32b_x32(tS + c, ra);
+                        tmem_ld_32x32b_x32(tS + c, ra);
                         tmem_ld_wait(ra);
 #pragma unroll
                         for (int i = 0; i < CW; ++i) s[i] = __uint_as_float(ra[i]);
@@ -985,24 +993,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int c = c0; c < c0 + NC; c += CW) {
                         if (NC > CW) load(c);
+                        uint32_t pk[CW / 2];
 #pragma unroll
-                        for (int q = 0; q < CW; q += 32) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float2 xa = fma2(make_float2(s[q + 2 * i], s[q + 2 * i + 1]), sc2, mneg);
-                                float2 xb = fma2(make_float2(s[q + 2 * i + 2], s[q + 2 * i + 3]), sc2, mneg);
-                                xa.x = fast_exp2(xa.x);
-                                xa.y = fast_exp2(xa.y);
-                                xb.x = fast_exp2(xb.x);
-                                xb.y = fast_exp2(xb.y);
-                                l0 = add2(l0, xa);
-                                l1 = add2(l1, xb);
-                                pk[i] = pack_bf16x2(xa.x, xa.y);
-                                pk[i + 1] = pack_bf16x2(xb.x, xb.y);
-                            }
-                            tmem_st_x16(tS + (c + q) / 2, pk);
+                        for (int i = 0; i < CW / 2; i += 2) {
+                            float2 xa = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mneg);
+                            float2 xb = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), sc2, mneg);
+                            xa.x = fast_exp2(xa.x);
+                            xa.y = fast_exp2(xa.y);
+                            xb.x = fast_exp2(xb.x);
+                            xb.y = fast_exp2(xb.y);
+                            l0 = add2(l0, xa);
+                            l1 = add2(l1, xb);
+                            pk[i] = pack_bf16x2(xa.x, xa.y);
+                            pk[i + 1] = pack_bf16x2(xb.x, xb.y);
                         }
+                        tmem_st_x16(tS + c / 2, pk);
                     }
                     if (kRep > 1) {
                         // P is zero in the other copies' columns.
