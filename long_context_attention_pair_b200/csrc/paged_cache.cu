@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, c
     const bool whole = (reinterpret_cast<uintptr_t>(kp) & 31u) == 0;
     float2 cs[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cs[j] = a.rotate ? turn_cos_sin_fast(pos, turn_of[8 * c + j]) : make_float2(1.f, 0.f);
+    for (int j = 0; j < 8; ++j) cs[j] = turn_cos_sin_fast(pos, turn_of[8 * c + j]);
     for (int h = 0; h < a.Hkv; ++h) {
         copy_async_wait<kStages - 1>();
         const uint4 *from = ring + h % kStages * 1024 + threadIdx.x;
@@ -102,10 +102,11 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, c
                     make_uint4(pack_bf16x2(f[4], g[4]), pack_bf16x2(f[5], g[5]), pack_bf16x2(f[6], g[6]), pack_bf16x2(f[7], g[7])), whole);
         } else {
             __nv_bfloat16 *dst = kp + natural_off(page, at, h, 0, P, a.Hkv, a.D);
+            // Un-rotated keys are copied: a turn by nothing would still mix in 0 * infinity.
             *reinterpret_cast<uint4 *>(dst + 8 * c) =
-                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                a.rotate ? make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])) : lo;
             *reinterpret_cast<uint4 *>(dst + H + 8 * c) =
-                make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
+                a.rotate ? make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])) : hi;
         }
         __nv_bfloat16 *dv = vp + natural_off(page, at, h, 0, P, a.Hkv, a.D);
         *reinterpret_cast<uint4 *>(dv + 8 * c) = v0;

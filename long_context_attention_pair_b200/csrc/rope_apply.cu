@@ -153,10 +153,6 @@ cudaError_t launch(const RopeTensor &q, const RopeTensor &k, const int32_t *posi
     per = per < 4 ? 4 : per;
     if (per > heads) per = heads;
     const size_t smem = V == 1 ? 0 : kStages * 2 * 256 * 16;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(rope_apply_kernel<E, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     rope_apply_kernel<E, V><<<dim3((unsigned)blocks, (unsigned)((heads + per - 1) / per)), 256, smem, s>>>(
         q, k, positions, (int)BT, (int)T, D, units, interleaved, scale, inverse ? -1.f : 1.f, per, rt);
     return cudaGetLastError();

@@ -31,7 +31,9 @@ def rope(x, positions, theta, *, rotary_dim=None, interleaved=False, scale=1.0, 
 def rope_slack(x, R, interleaved, scale, unit):
     """Largest |error| of each output element: its rounding (half a step of the type, `unit` relative to the
     value) is added by the caller; here the fp32 arithmetic, (|x| + |z|) * scale * 2^-20: the angle in half-turns
-    rounded to fp32 (pi * 2^-25), cos and sin to an ulp (2^-23), two products, their sum and the scale (each 2^-24)."""
+    rounded to fp32 (pi * 2^-25), cos and sin to an ulp (2^-23), two products, their sum and the scale (each 2^-24).
+    For bf16 the angle in radians (three roundings of at most pi: 3 * 2^-23, which moves cos and sin by |sin| and
+    |cos| times as much) and the hardware's cos and sin (2^-21.2): together with the products still below 2^-20."""
     y = x.double().abs()
     r = torch.arange(R // 2, device=x.device)
     i, j = (2 * r, 2 * r + 1) if interleaved else (r, r + R // 2)
