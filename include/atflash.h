@@ -354,7 +354,10 @@ int atflash_decode_paged_theta(const void *q, const void *kpages, const void *vp
  *
  * A slot past the sequence's table row, or a page id outside [0, num_pages), is
  * found on the device: the call records ATFLASH_ERR_BAD_PAGE in the device
- * status word, writes nothing to that slot and reads nothing from it.
+ * status word, writes nothing to that slot and reads nothing from it.  (Tree
+ * attention takes such a page's keys and values as zeros; a sequence whose length
+ * is negative, or whose nodes its table row has no room for, keeps its rows of out
+ * and lse as they were.)
  *
  * Tensors marked "strided" take a HOST array of three element strides {batch,
  * token, head}, read during the call (dims are contiguous); NULL means contiguous
@@ -435,7 +438,9 @@ int atflash_cache_append_theta(const void *k, const int64_t *k_strides, const vo
  *   workspace  device, 16-byte aligned, >= atflash_tree_decode_workspace_bytes();
  *              calls whose work overlaps on the GPU need one each.
  * What a key that a node does not see holds (infinities, NaN, stale slots) does
- * not reach that node.  Pages beyond seqlens[b] + counts[b] are not looked up.
+ * not reach that node.  A non-finite value in a committed slot, which every node
+ * sees, makes its dim non-finite in every node of that KV head (NaN, or the
+ * infinity).  Pages beyond seqlens[b] + counts[b] are not looked up.
  * Any Hq / Hkv; B*T*Hq <= 2^31 - 1.
  */
 size_t atflash_tree_decode_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
@@ -462,7 +467,7 @@ int atflash_tree_decode_paged_theta(const void *q, const int64_t *q_strides, con
  *               not moved (ATFLASH_ERR_BAD_PAGE in the device status word).
  *   accepted    device int32 [B], clamped to 0..M.
  *   new_seqlens NULL, or device int32 [B] written with seqlens[b] + accepted[b];
- *               must not be seqlens.
+ *               must not overlap seqlens, path, accepted or block_table.
  * The slots moved to must belong to one sequence each.
  */
 int atflash_cache_compact(void *kpages, void *vpages, const int32_t *block_table, const int32_t *seqlens,
@@ -473,7 +478,8 @@ int atflash_cache_compact(void *kpages, void *vpages, const int32_t *block_table
  * Page dst[e] receives the first tokens[e] tokens (clamped to 0..page_size; NULL:
  * all) of page src[e], K and V, for e < n (a forked sequence's last page, a pool
  * being compacted).  src and dst are device int32 [n].  A page must not be the
- * destination of two copies, nor of one and the source of another.
+ * destination of two copies, nor of one and the source of another.  A page holds
+ * fewer than 2^33 elements of K.
  */
 int atflash_cache_copy_pages(void *kpages, void *vpages, const int32_t *src, const int32_t *dst, const int32_t *tokens,
                              int n, int Hkv, int num_pages, int page_size, int D, int kv_layout, cudaStream_t stream);

@@ -72,6 +72,12 @@ struct BaseTheta {
     }
 };
 
+// Whether [a, a + na) and [b, b + nb) overlap.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? ATFLASH_OK : ATFLASH_ERR_CUDA; }
 
 }  // namespace
@@ -150,12 +156,16 @@ int atflash_cache_compact(void *kpages, void *vpages, const int32_t *block_table
                           const int32_t *path, const int32_t *accepted, int32_t *new_seqlens, int B, int M, int Hkv,
                           int max_pages, int num_pages, int page_size, int D, int kv_layout, cudaStream_t stream) {
     if (!kpages || !vpages || !block_table || !seqlens || !path || !accepted) return ATFLASH_ERR_INVALID_ARG;
-    if (new_seqlens == seqlens) return ATFLASH_ERR_INVALID_ARG;
     int rc = check_pool(Hkv, D, num_pages, page_size, kv_layout);
     if (rc != ATFLASH_OK) return rc;
     if ((rc = check_table(B, max_pages, page_size)) != ATFLASH_OK) return rc;
     if (M < 1 || (int64_t)B * Hkv * (D / 16) > INT32_MAX) return ATFLASH_ERR_INVALID_ARG;
     if (M > kCompactMaxPath) return ATFLASH_ERR_UNSUPPORTED;
+    // Other blocks still read the inputs when the first one writes its new length.
+    const int64_t n = 4 * (int64_t)B;
+    if (new_seqlens && (overlap(new_seqlens, n, seqlens, n) || overlap(new_seqlens, n, accepted, n) ||
+                        overlap(new_seqlens, n, path, n * M) || overlap(new_seqlens, n, block_table, n * max_pages)))
+        return ATFLASH_ERR_INVALID_ARG;
     if (!aligned(kpages, 16) || !aligned(vpages, 16)) return ATFLASH_ERR_ALIGNMENT;
     CompactArgs a{};
     a.kpages = kpages, a.vpages = vpages;
@@ -171,7 +181,8 @@ int atflash_cache_copy_pages(void *kpages, void *vpages, const int32_t *src, con
     if (!kpages || !vpages || !src || !dst || n < 1) return ATFLASH_ERR_INVALID_ARG;
     int rc = check_pool(Hkv, D, num_pages, page_size, kv_layout);
     if (rc != ATFLASH_OK) return rc;
-    if ((int64_t)page_size * Hkv * D / 8 > INT32_MAX) return ATFLASH_ERR_INVALID_ARG;
+    // Indices of 16-byte units, a round of loads past the last included, fit 32 bits.
+    if ((int64_t)page_size * Hkv * D / 8 > INT32_MAX / 2) return ATFLASH_ERR_INVALID_ARG;
     if (!aligned(kpages, 16) || !aligned(vpages, 16)) return ATFLASH_ERR_ALIGNMENT;
     CopyPagesArgs a{kpages, vpages, src, dst, tokens, n, Hkv, D, num_pages, page_size, kv_layout == ATFLASH_KV_PACKED,
                     device_status_word()};

@@ -126,3 +126,17 @@ def test_python_checks_come_before_the_library():
         atf._strided(torch.zeros(1, 2, 64, 4).transpose(2, 3), "q", (1, 2, 4, 64), torch.float32)
     with pytest.raises(ValueError, match="expanded"):
         atf._strided(torch.zeros(1, 1, 4, 64).expand(1, 2, 4, 64), "out_q", (1, 2, 4, 64), torch.float32, True)
+
+
+@pytest.mark.parametrize("name", ["lens", "acc", "path", "bt"])
+def test_new_lengths_must_not_overlap_an_input(L, name):
+    for new in (P, P + 4, P - 4):
+        a = {**GOOD, "lens": P + 4096, "acc": P + 8192, "path": P + 12288, "bt": P + 16384, "new": new, name: P}
+        assert L.atflash_cache_compact(*[a[x] for x in ORDER["cache_compact"].split()]) == -1
+
+
+def test_pages_beyond_32_bit_indices_are_refused(L):
+    a = {**GOOD, "page": 1 << 26, "Hkv": 4, "num_pages": 2}  # 2^32 units of 16 bytes
+    assert L.atflash_cache_copy_pages(*[a[x] for x in ORDER["cache_copy_pages"].split()]) == -1
+    a.update(page=1 << 24, Hkv=4)  # 2^30: an index and the round of loads after it reach 2^31
+    assert L.atflash_cache_copy_pages(*[a[x] for x in ORDER["cache_copy_pages"].split()]) == -1
