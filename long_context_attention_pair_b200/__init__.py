@@ -471,16 +471,23 @@ def _device_of(*tensors):
     return dev
 
 
-def _launch(fn, name, dev, stream, fresh, *args):
-    """fn(*args, stream) with ``dev`` current.  ``fresh``: tensors allocated for this call on
-    the current stream, kept reserved until ``stream`` is done with them."""
+def _new(stream, make, shape, dtype, device):
+    """make(shape) for a call on ``stream`` (None: the current one): allocated and filled on that
+    stream, behind nothing that the current one still has to do, and reserved for both."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
     torch = _torch()
-    raw = torch._C._cuda_getCurrentRawStream(dev)
-    if stream is not None and stream.cuda_stream != raw:
-        raw = stream.cuda_stream
-        for t in fresh:
-            if t is not None:
-                t.record_stream(stream)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _launch(fn, name, dev, stream, *args):
+    """fn(*args, stream) with ``dev`` current."""
+    torch = _torch()
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev:
         status = fn(*args, raw)
     else:
@@ -558,12 +565,10 @@ def rope_apply(q, k, positions, rope_base: float, *, rotary_dim=None, interleave
     B, T, Hq, D = q.shape
     dt, dtype = _dtype_code(q), q.dtype
     dev = _device_of(q, k, positions, out_q, out_k)
-    fresh = (None, None)
-    if out_q is None or (k is not None and out_k is None):
-        new_q = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device) if out_q is None else None
-        new_k = torch.empty(k.shape, dtype=dtype, device=q.device) if k is not None and out_k is None else None
-        fresh = (new_q, new_k)
-        out_q, out_k = (out_q if new_q is None else new_q), (out_k if new_k is None else new_k)
+    if out_q is None:
+        out_q = _new(stream, torch.empty, (B, T, Hq, D), dtype, q.device)
+    if k is not None and out_k is None:
+        out_k = _new(stream, torch.empty, k.shape, dtype, q.device)
     shape = (B, T, Hq, D)
     qp, qs = _strided(q, "q", shape, dtype)
     oqp, oqs = _strided(out_q, "out_q", shape, dtype, True)
@@ -576,7 +581,7 @@ def rope_apply(q, k, positions, rope_base: float, *, rotary_dim=None, interleave
         okp, oks = _strided(out_k, "out_k", shape, dtype, True)
     R = D if rotary_dim is None else int(rotary_dim)
     fn, name, rope = _rope_arg("atflash_rope_apply", rope_base, theta, R)
-    _launch(fn, name, dev, stream, fresh, qp, qs, kp, ks, oqp, oqs, okp, oks,
+    _launch(fn, name, dev, stream, qp, qs, kp, ks, oqp, oqs, okp, oks,
             _flat(positions, "positions", (B, T), torch.int32), B, T, Hq, Hkv, D, R, rope, float(scale),
             int(bool(interleaved)), int(bool(inverse)), dt)
     return out_q if k is None else (out_q, out_k)
@@ -603,7 +608,7 @@ def cache_append(k, v, kpages, vpages, block_table, seqlens, page_size: int, rop
     vp, vs = _strided(v, "v", (B, T, Hkv, D), bf16)
     max_pages = block_table.shape[-1]
     fn, name, rope = _rope_arg("atflash_cache_append", rope_base, theta, D)
-    _launch(fn, name, dev, stream, (), kp, ks, vp, vs, kpp, vpp, _flat(block_table, "block_table", (B, max_pages), i32),
+    _launch(fn, name, dev, stream, kp, ks, vp, vs, kpp, vpp, _flat(block_table, "block_table", (B, max_pages), i32),
             _flat(seqlens, "seqlens", (B,), i32), _flat(positions, "positions", (B, T), i32),
             _flat(counts, "counts", (B,), i32), B, T, Hkv, max_pages, num_pages, int(page_size), D, rope,
             int(bool(kcache_rotated)), lay)
@@ -642,20 +647,19 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
         if tree_mask.dtype != torch.bool and tree_mask.dtype != torch.uint8:
             raise TypeError("tree_mask must be uint8 or bool")
         mask = _flat(tree_mask, "tree_mask", (B, T, T), tree_mask.dtype)
-    new_out = new_lse = new_ws = None
     make = torch.empty if counts is None else torch.zeros
     if out is None:
-        out = new_out = make((B, T, Hq, D), dtype=out_dtype if out_dtype is not None else q.dtype, device=q.device)
+        out = _new(stream, make, (B, T, Hq, D), out_dtype if out_dtype is not None else q.dtype, q.device)
     if lse is None and return_lse:
-        lse = new_lse = make((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, make, (B, Hq, T), torch.float32, q.device)
     need = lib().atflash_tree_decode_workspace_bytes(B, T, Hq, Hkv, D)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = new_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, (max(need, 16),), torch.uint8, q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     max_pages = block_table.shape[-1]
     fn, name, rope = _rope_arg("atflash_tree_decode_paged", rope_base, theta, D)
-    _launch(fn, name, dev, stream, (new_out, new_lse, new_ws), qp, qs, kpp, vpp,
+    _launch(fn, name, dev, stream, qp, qs, kpp, vpp,
             _flat(block_table, "block_table", (B, max_pages), i32), _flat(seqlens, "seqlens", (B,), i32), mask,
             _flat(positions, "positions", (B, T), i32), _flat(counts, "counts", (B,), i32),
             _flat(out, "out", (B, T, Hq, D), out.dtype), _flat(lse, "lse", (B, Hq, T), torch.float32), B, T, Hq, Hkv,
@@ -670,18 +674,17 @@ def cache_compact(kpages, vpages, block_table, seqlens, path, accepted, page_siz
 
     For p < accepted[b] (int32 [B]) slot seqlens[b] + p receives what slot seqlens[b] +
     path[b, p] (int32 [B, M], M <= 1024) held before the call.  Returns new_seqlens =
-    seqlens + accepted (int32 [B], a new tensor unless given; not ``seqlens`` itself).
+    seqlens + accepted (int32 [B], a new tensor unless given; not one of the inputs).
     """
     torch = _torch()
     B, M = path.shape
     i32 = torch.int32
     dev = _device_of(kpages, vpages, block_table, seqlens, path, accepted, new_seqlens)
     lay, Hkv, D, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-    fresh = None
     if new_seqlens is None:
-        new_seqlens = fresh = torch.empty((B,), dtype=i32, device=seqlens.device)
+        new_seqlens = _new(stream, torch.empty, (B,), i32, seqlens.device)
     max_pages = block_table.shape[-1]
-    _launch(lib().atflash_cache_compact, "atflash_cache_compact", dev, stream, (fresh,), kpp, vpp,
+    _launch(lib().atflash_cache_compact, "atflash_cache_compact", dev, stream, kpp, vpp,
             _flat(block_table, "block_table", (B, max_pages), i32), _flat(seqlens, "seqlens", (B,), i32),
             _flat(path, "path", (B, M), i32), _flat(accepted, "accepted", (B,), i32),
             _flat(new_seqlens, "new_seqlens", (B,), i32), B, M, Hkv, max_pages, num_pages, int(page_size), D, lay)
@@ -696,7 +699,7 @@ def cache_copy_pages(kpages, vpages, src, dst, page_size: int, *, tokens=None, k
     n, i32 = src.numel(), torch.int32
     dev = _device_of(kpages, vpages, src, dst, tokens)
     lay, Hkv, D, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-    _launch(lib().atflash_cache_copy_pages, "atflash_cache_copy_pages", dev, stream, (), kpp, vpp,
+    _launch(lib().atflash_cache_copy_pages, "atflash_cache_copy_pages", dev, stream, kpp, vpp,
             _flat(src, "src", (n,), i32), _flat(dst, "dst", (n,), i32), _flat(tokens, "tokens", (n,), i32), n, Hkv,
             num_pages, int(page_size), D, lay)
 

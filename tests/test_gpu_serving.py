@@ -557,3 +557,37 @@ def test_tree_two_streams_at_once_and_again():
         torch.cuda.synchronize()
         for (o, l), (c, q, kw, out, lse, call) in zip(outs, runs):
             assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_append_unrotated_copies_every_bit():
+    """Keys stored un-rotated keep infinities, NaN and signed zeros, and do not spread them to their partners."""
+    B, T, Hkv, D, page = 1, 70, 2, 64, 64
+    k, v = randn((B, T, Hkv, D), 231), randn((B, T, Hkv, D), 232)
+    k[:, 3, :, 5], k[:, 4, :, 40], k[:, 5, :, 9], k[:, 6, :, 10] = math.inf, -math.inf, math.nan, -0.0
+    k[:, 6, :, 42] = -1.0
+    c = R.Cache(B, 2, page, Hkv, D, False, 233, fill=0.0)
+    atf.cache_append(k, v, c.kpages, c.vpages, c.block_table, ints([9]), page, 1e4, kcache_rotated=False)
+    slots = torch.arange(9, 9 + T, device="cuda")
+    where, at = c.block_table[0].long()[slots // page], slots % page
+    assert torch.equal(c.kpages[where, at].view(torch.int16), k[0].view(torch.int16))
+    assert torch.equal(c.vpages[where, at].view(torch.int16), v[0].view(torch.int16))
+
+
+def test_a_call_on_another_stream_does_not_wait_for_the_current_one():
+    """Outputs, zeros behind the last node and workspaces of a call with stream= belong to that stream: work still queued
+    on the current one neither holds them back nor overwrites them."""
+    c, q, kw, want, wlse, call = run_tree(128, 8, 2, 64, True, [300, 90], 8, [8, 3], "tree", 8.0, seed=241)
+    lens, other = ints([300, 90]), torch.cuda.Stream()
+    path, acc, pos = ints([[0, 1], [0, 1]]), ints([2, 1]), ints([[5] * 8] * 2)
+    x = torch.ones((4096, 4096), device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        x = x @ x * 0.0
+    out, lse = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, lens, 64, 1e4, 8.0, return_lse=True, stream=other, **kw)
+    turned = atf.rope_apply(q, None, pos, 1e4, stream=other)
+    new = atf.cache_compact(c.kpages, c.vpages, c.block_table, lens, path, acc, 64, kv_layout="PACKED", stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, :3], want[1, :3]) and not bool(out[1, 3:].any())
+    assert torch.equal(lse[0], wlse[0]) and torch.equal(lse[1, :, :3], wlse[1, :, :3])
+    assert torch.equal(turned, atf.rope_apply(q, None, pos, 1e4))
+    assert new.tolist() == [302, 91]
