@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < ST; ++s) {
                 mbar_init(&ctl->k_full[s], 1);
                 mbar_init(&ctl->k_ready[s], 1);
-                mbar_init(&ctl->k_empty[s], 1 + 1 + 4);  // QK, the fix-up warp, the set's softmax warps
+                mbar_init(&ctl->k_empty[s], 1 + 4);  // QK, the set's softmax warps
                 mbar_init(&ctl->v_full[s], 1);
                 mbar_init(&ctl->v_tail[s], 1);
                 mbar_init(&ctl->v_ready[s], 2);
@@ -552,13 +552,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t m0 = (int64_t)j * kBN;
                 if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 43))) break;
                 const int4 bd = ctl->band[it % 8];
-                __syncwarp();
+                uint8_t *kst = sK + st * F::TileBytes;
+                // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
+                const int z = bd.y % kPer;
+                if (z) {
+                    const int c = bd.y / kPer;
+#pragma unroll
+                    for (int e = 0; e < kBN; e += 32) {
+                        if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + e, 0), kst + c * 4096 + sw32_off(lane + e, 4), z);
+                        else {
+                            for (int half = 0; half < 2; ++half) {
+                                const int d = 16 * c + half * H;
+                                uint8_t *u0 = kst + sw128_off(lane + e, d), *u1 = kst + sw128_off(lane + e, d + 8);
+                                zero_words(u0, u1, z / 2);
+                                if (z & 1) *reinterpret_cast<uint16_t *>((z < 8 ? u0 : u1) + (z & 6) * 2) = 0;
+                            }
+                        }
+                    }
+                }
                 if (!(bd.w & kBandFix)) {
-                    // Seen: without this, the stage could be reloaded before this warp looks at it.
-                    if (lane == 0) mbar_arrive(&ctl->k_empty[st]);
+                    if (z) fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
                     continue;
                 }
-                uint8_t *kst = sK + st * F::TileBytes;
                 constexpr int kK = kBN / 32;  // this lane's keys: lane, lane + 32, ..
                 const bool prefix = m0 + kBN <= g.L;
                 int kp[kK];
@@ -608,10 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ctl->chunks[cb] = bd.x < bd.y ? 0xfu : chunks;
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ctl->k_ready[st]);
-                    mbar_arrive(&ctl->k_empty[st]);
-                }
+                if (lane == 0) mbar_arrive(&ctl->k_ready[st]);
             }
         }
     } else if (warp >= kTail) {
@@ -687,44 +701,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------- QK issuer
         const uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
         const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
-        uint32_t fixed = 0;  // phase bit of k_ready per stage
         while (ok && runs.next(wc, ok)) {
             const int ntile = runs.now().ntile;
             runs.done(lane);
             if (!(ok = wait(&ctl->q_ready, (runs.n - 1) & 1, wc, 46))) break;
             for (int j = 0; ok && j < ntile; ++j, ++it) {
                 const int st = it % ST, buf = it % kBufs;
-                if (!(ok = wait(&ctl->k_full[st], (it / ST) & 1, wc, 47))) break;
+                if (!(ok = wait(&ctl->k_ready[st], (it / ST) & 1, wc, 48))) break;
                 const int4 bd = ctl->band[it % 8];
-                // Pairs below rs that share its K-step are pruned for every cell: zeroed whole.
-                const int z = bd.y % kPer;
-                if (z) {
-                    uint8_t *kst = sK + st * F::TileBytes;
-                    const int c = bd.y / kPer;
-#pragma unroll
-                    for (int e = 0; e < kBN; e += 32) {
-                        if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + e, 0), kst + c * 4096 + sw32_off(lane + e, 4), z);
-                        else {
-                            for (int half = 0; half < 2; ++half) {
-                                const int d = 16 * c + half * H;
-                                uint8_t *u0 = kst + sw128_off(lane + e, d), *u1 = kst + sw128_off(lane + e, d + 8);
-                                zero_words(u0, u1, z / 2);
-                                if (z & 1) *reinterpret_cast<uint16_t *>((z < 8 ? u0 : u1) + (z & 6) * 2) = 0;
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (bd.w & kBandFix) {
-                    if (!(ok = wait(&ctl->k_ready[st], (fixed >> st) & 1, wc, 48))) break;
-                    fixed ^= 1u << st;
-                }
                 if (it >= kBufs && !(ok = wait(&ctl->o_done[buf], (it / kBufs - 1) & 1, wc, 49))) break;
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + buf * kBN;
                     uint32_t acc = 0;
+#pragma unroll 1
                     for (int c = bd.y / kPer; c < H / kPer; ++c) {
 #pragma unroll
                         for (int part = 0; part < (kPacked ? 1 : 2); ++part) {
@@ -769,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&ctl->p_full[buf], (it / kBufs) & 1, wc, 52))) break;
                 if (lane == 0) {
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < kBN / 16; ++kk) {
                         const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
                         umma_bf16_ts(tmem + F::TmemO, tmem + buf * kBN + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
