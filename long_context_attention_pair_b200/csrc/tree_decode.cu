@@ -40,11 +40,21 @@
 // V's own), which moves an output by at most 2^-8 of sum p |v|; sums, maxima and
 // O are fp32.
 //
-// Warps: the softmax warps, then one each for loading K, issuing QK, the fix-up of
-// boundary pairs (staged, and zeroed in K), issuing PV, loading V and scheduling (it
-// publishes the runs of tiles through a ring), and two for the tails (mask bits of
-// tiles with nodes, V behind the last node cleared).  Every mbarrier wait is bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its
-// copies and MMAs finish and exits.
+// Warps: the softmax warps, then one each for loading K, issuing QK, the fix-up of K
+// (boundary pairs staged, they and pruned pairs zeroed), issuing PV, loading V and
+// scheduling (it publishes the runs of tiles through a ring), and two for the tails (mask
+// bits of tiles with nodes, V behind the last node cleared).  Every mbarrier wait is
+// bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its copies and MMAs finish
+// and exits.
+//
+// What bounds it.  A key tile takes 2 200 to 2 600 clocks: two K stages (D = 128) whose
+// cycle is copy issue 900, arrival 1 300 to 1 900, fix-up 400, QK 1 200 to 1 600 and
+// release 300.  Ten roles share the instruction caches, so short loops beat unrolled ones
+// everywhere (the MMA issue loops: 68 -> 61 us on 8 ragged sequences of up to 8192 keys
+// with trees of 16).  A CTA's first P comes about 20 000 clocks after its start, through
+// code that is fetched cold, which bounds small calls (24 us).  4 sequences of 64K keys,
+// one token each, no window: 106 us, 0.77 of the copy rate; 2 of 128K keys with trees of
+// 64 nodes (448 rows per KV head): 340 us, 570 TFLOP/s without the second part of q~.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -67,7 +77,7 @@ constexpr int kLaunchRegs = 128, kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
-constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences)
+constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences when they took 71)
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -523,10 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *dst = (v ? sV : sK) + st * F::TileBytes + (kPacked && !v ? u * 4096 + hf * 2048 : u * 16384 + hf * 8192);
                 const bool mine = issue && (kPacked && !v ? u >= ca && u < C : u < D / 64);
                 const int z = (pg * sh.Hkv + g.h) * C + u;
+                // (Entry it % 8 is free: the wait for tile it - 1 has shown the PV of it - 8.)
+                if (!v && lane == 0) ctl->band[it % 8] = make_band<D, kPacked>(r_lo, r_full, g.pmin != g.pmax);
                 if (!(ok = wait(&empty[st], ((it / ST) & 1) ^ 1, wc, v ? 42 : 41))) break;
                 if (lane == 0) {
                     if (v && m0 + kBN > g.L) mbar_arrive(&ctl->v_tail[st]);  // a tile with nodes is on its way
-                    if (!v) ctl->band[it % 8] = make_band<D, kPacked>(r_lo, r_full, g.pmin != g.pmax);
                     mbar_expect_tx(&full[st], bytes);
                 }
                 __syncwarp();
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int z = bd.y % kPer;
                 if (z) {
                     const int c = bd.y / kPer;
-#pragma unroll
+#pragma unroll 1
                     for (int e = 0; e < kBN; e += 32) {
                         if constexpr (kPacked) zero_words(kst + c * 4096 + sw32_off(lane + e, 0), kst + c * 4096 + sw32_off(lane + e, 4), z);
                         else {
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint32_t k0 = sKa + st * F::TileBytes, d = tmem + buf * kBN;
                     uint32_t acc = 0;
-#pragma unroll 1
+#pragma unroll 1  // (a short loop: see the head of this file)
                     for (int c = bd.y / kPer; c < H / kPer; ++c) {
 #pragma unroll
                         for (int part = 0; part < (kPacked ? 1 : 2); ++part) {
