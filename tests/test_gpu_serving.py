@@ -259,6 +259,17 @@ def test_tree_many_tiles_in_a_row(packed, D, Hq, Hkv, page, lens, T, k):
 
 
 @pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv,page,lens,T,counts,kind,k", [
+    (128, 8, 1, 64, [300, 40], 300, [300, 150], "tree", 2.0),  # 2400 rows: three groups of seven row tiles, the last not full
+    (64, 16, 2, 128, [1100, 7, 64], 129, [129, 128, 1], "any", 1.0),  # 1032 rows: two groups, of which one sequence has one row tile
+    (64, 32, 1, 64, [700], 65, None, "chain", 4.0),  # 2080 rows: three groups of six
+])
+def test_tree_of_many_rows(packed, D, Hq, Hkv, page, lens, T, counts, kind, k):
+    # More rows than the row tiles that walk the keys together: several groups of them, some without rows.
+    run_tree(D, Hq, Hkv, page, packed, lens, T, counts, kind, k, seed=321)
+
+
+@pytest.mark.parametrize("packed", [False, True])
 def test_tree_every_key_counts_once(packed):
     # Uniform weights (queries of zeros) over one-hot values by key tile: output dim d is the share of the keys
     # in tiles d mod D, which one lost or doubled run of keys would change.
