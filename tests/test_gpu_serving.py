@@ -270,6 +270,18 @@ def test_tree_of_many_rows(packed, D, Hq, Hkv, page, lens, T, counts, kind, k):
 
 
 @pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("idle", [0, 40])
+def test_tree_of_many_sequences(packed, idle):
+    # More sequences than a warp has lanes, the first `idle` of them without a node.
+    B, T = 75, 3
+    lens = [(i * 137) % 700 for i in range(B)]
+    counts = [0 if b < idle else (b * 5) % (T + 2) for b in range(B)]
+    run_tree(64, 4, 2, 64, packed, lens, T, counts, "tree", 1.0, seed=331)
+    if not idle:
+        run_tree(128, 2, 1, 64, packed, lens, T, None, "chain", 4.0, seed=341)
+
+
+@pytest.mark.parametrize("packed", [False, True])
 def test_tree_every_key_counts_once(packed):
     # Uniform weights (queries of zeros) over one-hot values by key tile: output dim d is the share of the keys
     # in tiles d mod D, which one lost or doubled run of keys would change.
