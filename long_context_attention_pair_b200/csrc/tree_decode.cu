@@ -547,11 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (!ok) {
-            // Let every copy land before the CTA exits: the tiles before `it` are issued.
-            for (int x = it > ST ? it - ST : 0; x < it; ++x)
-                wait_drain(&full[x % ST], (x / ST) & 1, atflash_drain_limit_ns(a.limit_ns));
-        }
+        // Let every copy land before the CTA exits: the tiles before `it` are issued.  Also after the
+        // last run: another warp's wait may run out before anyone has waited for this warp's last tiles.
+        for (int x = it > ST ? it - ST : 0; x < it; ++x)
+            wait_drain(&full[x % ST], (x / ST) & 1, atflash_drain_limit_ns(a.limit_ns));
     } else if (warp == kFix) {
         // ------------------------------------------------ boundary pairs of K
         while (ok && runs.next(wc, ok)) {

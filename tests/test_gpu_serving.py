@@ -614,3 +614,34 @@ def test_a_call_on_another_stream_does_not_wait_for_the_current_one():
     assert torch.equal(lse[0], wlse[0]) and torch.equal(lse[1, :, :3], wlse[1, :, :3])
     assert torch.equal(turned, atf.rope_apply(q, None, pos, 1e4))
     assert new.tolist() == [302, 91]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,T", [(64, 4, 3), (128, 8, 40)])
+def test_tree_waits_that_run_out_are_reported_and_leave_the_gpu_usable(packed, D, Hq, T):
+    # Every sequence is about one CTA's run, its nodes in the last of 161 tiles: the warps that take the
+    # nodes' tiles wait through the whole run, far beyond a limit of 1 us.
+    B, page, L = 148, 256, 160 * 128 + 5
+    c = R.Cache(B, L // page + 1, page, 1, D, packed, 411)
+    c.kpages.copy_(randn(c.kpages.shape, 412))
+    c.vpages.copy_(randn(c.vpages.shape, 413))
+    q, lens = randn((B, T, Hq, D), 414), ints([L] * B)
+    small = run_tree(D, Hq, 1, 64, packed, [200, 3], T, None, "tree", 4.0, seed=415)
+    call = lambda: atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, lens, page, 1e4, 8.0, kv_layout=c.layout,  # noqa: E731
+                                         return_lse=True)
+    want, wlse = call()
+    torch.cuda.synchronize()
+    assert atf.device_status() == 0
+    try:
+        atf.set_wait_limit_ms(0.001)
+        call()
+        assert atf.device_status() == atf.ERR_TIMEOUT
+        out, lse = torch.empty_like(small[3]), torch.empty_like(small[4])
+        small[5](out, lse)  # producers that are done early, whichever of the other waits runs out
+        assert atf.device_status() in (0, atf.ERR_TIMEOUT)
+    finally:
+        atf.set_wait_limit_ms(2000.0)
+    got, glse = call()
+    assert torch.equal(got, want) and torch.equal(glse, wlse)
+    small[5](out, lse)
+    assert torch.equal(out, small[3]) and torch.equal(lse, small[4])
