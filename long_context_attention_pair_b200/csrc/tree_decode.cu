@@ -1161,8 +1161,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    // Teardown: every tensor-core operation must be complete before TMEM is freed.
+    // Teardown: every tensor-core operation must be complete before TMEM is freed.  (A softmax warp
+    // that gave up between its stores to TMEM and their wait has them in flight here.)
+    if (warp < kSoft) tmem_st_wait();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     if (warp == kPv && lane == 0) umma_commit(&ctl->drain);
     if (warp == kQk) {
         if (lane == 0) {
