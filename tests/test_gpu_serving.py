@@ -645,3 +645,21 @@ def test_tree_waits_that_run_out_are_reported_and_leave_the_gpu_usable(packed, D
     assert torch.equal(got, want) and torch.equal(glse, wlse)
     small[5](out, lse)
     assert torch.equal(out, small[3]) and torch.equal(lse, small[4])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_append_of_the_most_tokens_that_a_call_takes(packed):
+    # 2^31 - 1 tokens (one, repeated by strides of zero) of which five are live: the last block's threads reach index
+    # 2^31 - 1, one past the last token.
+    Hkv, D, page, T, live, at = 1, 128, 64, (1 << 31) - 1, 5, 61
+    k, v = randn((1, 1, Hkv, D), 421), randn((1, 1, Hkv, D), 422)
+    c = R.Cache(1, 2, page, Hkv, D, packed, 423)
+    atf.cache_append(k.expand(1, T, Hkv, D), v.expand(1, T, Hkv, D), c.kpages, c.vpages, c.block_table, ints([at]), page, 1e4,
+                     counts=ints([live]), kv_layout=c.layout)
+    slots = at + torch.arange(live, device="cuda")
+    gk, gv = c.read(0, slots)
+    x = k.expand(1, live, Hkv, D)
+    ref = R.rope(x, slots[None], R.theta_of(1e4, D))
+    R.close(gk[None], ref, ref.abs() * 2.0 ** -8 + R.rope_slack(x, D, False, 1.0, 0), "key")
+    assert torch.equal(gv, v[0].expand(live, Hkv, D))
+    assert int((~torch.isnan(c.kpages)).sum()) == int((~torch.isnan(c.vpages)).sum()) == live * Hkv * D
