@@ -629,10 +629,12 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
     seqlens[b] committed slots and the nodes j with tree_mask[b, i, j] ([B, T, T]
     uint8 or bool; j <= i by default), whose keys and values ``cache_append`` put in
     slots seqlens[b] + j.  Only the first counts[b] nodes (all T by default) take part;
-    other rows of ``out`` are left as they were (zeros when allocated here).  Returns
-    out [B, T, Hq, D]; with ``return_lse`` or an ``lse`` buffer, (out, lse [B, Hq, T]
-    fp32).  A node that sees nothing gets 0 and -inf.  ``workspace``:
-    ``tree_decode_workspace_bytes`` bytes, not shared by calls that overlap.
+    other rows of ``out`` and ``lse``, and those of a sequence whose length is negative or
+    does not fit its table row (``device_status`` -7), are left as they were (zeros when
+    allocated here).  Returns out [B, T, Hq, D]; with ``return_lse`` or an ``lse`` buffer,
+    (out, lse [B, Hq, T] fp32).  A node that sees nothing gets 0 and -inf.  ``workspace``:
+    ``tree_decode_workspace_bytes`` bytes, not shared by calls that overlap; allocated
+    here when absent or smaller.
     """
     torch = _torch()
     B, T, Hq, D = q.shape
@@ -647,11 +649,11 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
         if tree_mask.dtype != torch.bool and tree_mask.dtype != torch.uint8:
             raise TypeError("tree_mask must be uint8 or bool")
         mask = _flat(tree_mask, "tree_mask", (B, T, T), tree_mask.dtype)
-    make = torch.empty if counts is None else torch.zeros
+    # (Zeros also without counts: a sequence that the call refuses keeps its rows.)
     if out is None:
-        out = _new(stream, make, (B, T, Hq, D), out_dtype if out_dtype is not None else q.dtype, q.device)
+        out = _new(stream, torch.zeros, (B, T, Hq, D), out_dtype if out_dtype is not None else q.dtype, q.device)
     if lse is None and return_lse:
-        lse = _new(stream, make, (B, Hq, T), torch.float32, q.device)
+        lse = _new(stream, torch.zeros, (B, Hq, T), torch.float32, q.device)
     need = lib().atflash_tree_decode_workspace_bytes(B, T, Hq, Hkv, D)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = _new(stream, torch.empty, (max(need, 16),), torch.uint8, q.device)

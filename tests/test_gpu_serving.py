@@ -663,3 +663,36 @@ def test_append_of_the_most_tokens_that_a_call_takes(packed):
     R.close(gk[None], ref, ref.abs() * 2.0 ** -8 + R.rope_slack(x, D, False, 1.0, 0), "key")
     assert torch.equal(gv, v[0].expand(live, Hkv, D))
     assert int((~torch.isnan(c.kpages)).sum()) == int((~torch.isnan(c.vpages)).sum()) == live * Hkv * D
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,lens,T", [(64, 4, [300, 290], 8), (128, 6, [700, 20], 30)])
+def test_tree_bad_lengths_keep_their_rows_and_bad_pages_are_zeros(packed, D, Hq, lens, T):
+    Hkv, page = 2, 64
+    c, q, kw, out, lse, call = run_tree(D, Hq, Hkv, page, packed, lens, T, None, "tree", 4.0, seed=431)
+    args = (page, 1e4, 4.0)
+    room = c.block_table.shape[1] * page
+    for bad in (-1, -(1 << 31), room - T + 1, (1 << 31) - 1):
+        # Rows of the caller's, and rows made by the call from memory that held something else.
+        o, l = torch.full_like(out, 3.0), torch.full_like(lse, 3.0)
+        atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints([bad, lens[1]]), *args, out=o, lse=l, **kw)
+        assert atf.device_status() == atf.ERR_BAD_PAGE
+        assert bool((o[0] == 3.0).all()) and bool((l[0] == 3.0).all())
+        assert torch.equal(o[1], out[1]) and torch.equal(l[1], lse[1])
+        junk = [torch.full_like(x, 5.0) for x in (out, out, lse, lse)]
+        del junk
+        o, l = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints([bad, lens[1]]), *args, return_lse=True, **kw)
+        assert atf.device_status() == atf.ERR_BAD_PAGE
+        assert not bool(o[0].any()) and not bool(l[0].any())
+        assert torch.equal(o[1], out[1]) and torch.equal(l[1], lse[1])
+    # A page outside the pool: its keys and values count as zeros.
+    zeros = c.clone()
+    zeros.write(0, torch.arange(2 * page, 3 * page, device="cuda"), *(torch.zeros((page, Hkv, D), dtype=torch.bfloat16, device="cuda"),) * 2)
+    ref, rlse, err, lerr = R.tree(q, zeros, lens, [T, T], kw["positions"], kw["tree_mask"], R.theta_of(1e4, D), 4.0)
+    for bad in (c.n, -1, (1 << 31) - 1):
+        table = c.block_table.clone()
+        table[0, 2] = bad
+        o, l = atf.tree_decode_paged(q, c.kpages, c.vpages, table, ints(lens), *args, return_lse=True, **kw)
+        assert atf.device_status() == atf.ERR_BAD_PAGE
+        R.close(o, ref, err.expand_as(ref) + ref.abs() * HALF[torch.bfloat16], "out")
+        R.close(l, rlse, lerr, "lse")
