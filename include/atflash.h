@@ -354,10 +354,10 @@ int atflash_decode_paged_theta(const void *q, const void *kpages, const void *vp
  *
  * A slot past the sequence's table row, or a page id outside [0, num_pages), is
  * found on the device: the call records ATFLASH_ERR_BAD_PAGE in the device
- * status word, writes nothing to that slot and reads nothing from it.  (Tree
- * attention takes such a page's keys and values as zeros; a sequence whose length
- * is negative, or whose nodes its table row has no room for, keeps its rows of out
- * and lse as they were.)
+ * status word, writes nothing to that slot and reads nothing from it.  A sequence
+ * whose length is negative has no slots.  (Tree attention takes such a page's keys
+ * and values as zeros; a sequence whose length is negative, or whose nodes its
+ * table row has no room for, keeps its rows of out and lse as they were.)
  *
  * Tensors marked "strided" take a HOST array of three element strides {batch,
  * token, head}, read during the call (dims are contiguous); NULL means contiguous

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a, c
     if ((int)threadIdx.x < H) turn_of[threadIdx.x] = rt.turn[threadIdx.x];
     __syncthreads();
     if (!live) return;
-    const int64_t slot = (int64_t)a.seqlens[b] + i;
+    const int64_t L = a.seqlens[b], slot = L < 0 ? -1 : L + i;  // of a negative length no slot exists
     const int page = page_of(a.pk, b, slot, a.status);
     if (page < 0) {
         copy_async_wait<0>();  // nothing of this thread's is in flight when it leaves
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(128) cache_compact_kernel(const CompactArgs a,
     uint4 *kp = static_cast<uint4 *>(a.kpages), *vp = static_cast<uint4 *>(a.vpages);
     for (int p = threadIdx.x; p < n; p += blockDim.x) {
         const int node = a.path[(size_t)b * a.M + p];
-        const int64_t src = node >= 0 ? L + node : -1;
+        const int64_t src = node >= 0 && L >= 0 ? L + node : -1;
         int2 f = make_int2(page_of(a.pk, b, src, a.status), 0), t = make_int2(page_of(a.pk, b, L + p, a.status), 0);
         if (f.x < 0 || t.x < 0) f.x = -1;  // a token whose source (or target) does not exist is not moved
         else f.y = (int)((uint32_t)src % (uint32_t)P), t.y = (int)((uint32_t)(L + p) % (uint32_t)P);

@@ -696,3 +696,25 @@ def test_tree_bad_lengths_keep_their_rows_and_bad_pages_are_zeros(packed, D, Hq,
         assert atf.device_status() == atf.ERR_BAD_PAGE
         R.close(o, ref, err.expand_as(ref) + ref.abs() * HALF[torch.bfloat16], "out")
         R.close(l, rlse, lerr, "lse")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_negative_length_moves_nothing(packed):
+    # Slots that a negative length and a token's index add up to belong to the committed prefix.
+    B, T, Hkv, D, page = 2, 10, 2, 64, 64
+    c = R.Cache(B, 2, page, Hkv, D, packed, 441)
+    c.kpages.copy_(randn(c.kpages.shape, 442))
+    c.vpages.copy_(randn(c.vpages.shape, 443))
+    k, v = randn((B, T, Hkv, D), 444), randn((B, T, Hkv, D), 445)
+    for n in (-3, -9, -(1 << 31)):
+        got, want = c.clone(), c.clone()
+        atf.cache_append(k, v, got.kpages, got.vpages, c.block_table, ints([n, 7]), page, 1e4, kv_layout=c.layout)
+        assert atf.device_status() == atf.ERR_BAD_PAGE
+        atf.cache_append(k[1:], v[1:], want.kpages, want.vpages, c.block_table[1:], ints([7]), page, 1e4, kv_layout=c.layout)
+        assert torch.equal(got.kpages, want.kpages) and torch.equal(got.vpages, want.vpages)
+        got, want = c.clone(), c.clone()
+        path = ints([[4, 12, 5, 11, 9, 3]] * 2)
+        atf.cache_compact(got.kpages, got.vpages, c.block_table, ints([n, 7]), path, ints([6, 6]), page, kv_layout=c.layout)
+        assert atf.device_status() == atf.ERR_BAD_PAGE
+        atf.cache_compact(want.kpages, want.vpages, c.block_table[1:], ints([7]), path[1:], ints([6]), page, kv_layout=c.layout)
+        assert torch.equal(got.kpages, want.kpages) and torch.equal(got.vpages, want.vpages)
