@@ -695,15 +695,16 @@ def cache_compact(kpages, vpages, block_table, seqlens, path, accepted, page_siz
 
 def cache_copy_pages(kpages, vpages, src, dst, page_size: int, *, tokens=None, kv_layout: str = "NHD", stream=None):
     """Page dst[e] receives the first tokens[e] tokens (all by default) of page src[e], K and
-    V, in place (int32 [n] each).  A page must not be the destination of two copies, nor
-    of one and the source of another."""
+    V, in place (int32 [n] each; nothing is done for n = 0).  A page must not be the
+    destination of two copies, nor of one and the source of another."""
     torch = _torch()
     n, i32 = src.numel(), torch.int32
     dev = _device_of(kpages, vpages, src, dst, tokens)
     lay, Hkv, D, num_pages, kpp, vpp = _pools(kpages, vpages, page_size, kv_layout, torch.bfloat16)
-    _launch(lib().atflash_cache_copy_pages, "atflash_cache_copy_pages", dev, stream, kpp, vpp,
-            _flat(src, "src", (n,), i32), _flat(dst, "dst", (n,), i32), _flat(tokens, "tokens", (n,), i32), n, Hkv,
-            num_pages, int(page_size), D, lay)
+    sp, dp, tp = (_flat(t, name, (n,), i32) for t, name in ((src, "src"), (dst, "dst"), (tokens, "tokens")))
+    if n:
+        _launch(lib().atflash_cache_copy_pages, "atflash_cache_copy_pages", dev, stream, kpp, vpp, sp, dp, tp, n, Hkv,
+                num_pages, int(page_size), D, lay)
 
 
 def device_status(clear: bool = True) -> int:

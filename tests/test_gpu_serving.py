@@ -718,3 +718,18 @@ def test_a_negative_length_moves_nothing(packed):
         assert atf.device_status() == atf.ERR_BAD_PAGE
         atf.cache_compact(want.kpages, want.vpages, c.block_table[1:], ints([7]), path[1:], ints([6]), page, kv_layout=c.layout)
         assert torch.equal(got.kpages, want.kpages) and torch.equal(got.vpages, want.vpages)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_copying_no_pages_changes_nothing(packed):
+    c = R.Cache(1, 2, 64, 2, 64, packed, 451)
+    c.kpages.copy_(randn(c.kpages.shape, 452))
+    c.vpages.copy_(randn(c.vpages.shape, 453))
+    want, none = c.clone(), ints([])
+    atf.cache_copy_pages(c.kpages, c.vpages, none, none, 64, kv_layout=c.layout)
+    atf.cache_copy_pages(c.kpages, c.vpages, none, none, 64, tokens=none, kv_layout=c.layout)
+    assert torch.equal(c.kpages, want.kpages) and torch.equal(c.vpages, want.vpages)
+    for bad in (dict(src=ints([1])), dict(tokens=ints([3])), dict(dst=none.long())):  # still refused
+        a = {**dict(src=none, dst=none, tokens=None), **bad}
+        with pytest.raises((ValueError, TypeError)):
+            atf.cache_copy_pages(c.kpages, c.vpages, a["src"], a["dst"], 64, tokens=a["tokens"], kv_layout=c.layout)
