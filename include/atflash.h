@@ -139,13 +139,14 @@ int atflash_prefill_ex(const void *q, const void *k, const void *v, void *out, i
  * keys, and the probabilities P, to bf16.  Over a row that sees few keys those
  * roundings do not average out (seeded sweeps measured errors up to 1.06e-2 on
  * rows of 4-16 keys, against below 4e-3 on rows of more than 128 keys), so
- * every bf16 call recomputes, after its tensor-core kernel, each row that sees
- * at most 128 keys in fp32 on CUDA cores from the un-rotated inputs, by the
+ * every bf16 prefill and decode recomputes, after its tensor-core kernel, each row
+ * that sees at most 128 keys in fp32 on CUDA cores from the un-rotated inputs, by the
  * method's plain definition ("The idea": RoPE, the per-pair window, softmax,
  * P.V), and overwrites that row's output and log-sum-exp: the first 128-row
  * tile of every prefill sequence, every query tile of a block selection whose
  * mask selects no earlier key tile, and every decode sequence of at most 128
- * tokens.
+ * tokens.  (atflash_tree_decode_paged, below, keeps such rows' queries and
+ * probabilities to 2^-16 in its tensor-core kernel instead.)
  *
  * atflash_prefill_short_rows is that step on its own, for callers that run
  * atflash_rope_pack + atflash_prefill_packed themselves: same q, k, v (the
@@ -441,6 +442,10 @@ int atflash_cache_append_theta(const void *k, const int64_t *k_strides, const vo
  * not reach that node.  A non-finite value in a committed slot, which every node
  * sees, makes its dim non-finite in every node of that KV head (NaN, or the
  * infinity).  Pages beyond seqlens[b] + counts[b] are not looked up.
+ * Accuracy: scores to about 2^-16 of the sum of their terms' sizes; probabilities to
+ * 2^-16 where out_dtype is ATFLASH_F32 and for sequences of at most 128 committed
+ * tokens (which hold every row that sees at most 128 keys), otherwise rounded to
+ * bf16 once, which moves an output by at most 2^-8 of sum p |v|; sums in fp32.
  * Any Hq / Hkv; B*T*Hq <= 2^31 - 1.
  */
 size_t atflash_tree_decode_workspace_bytes(int B, int T, int Hq, int Hkv, int D);

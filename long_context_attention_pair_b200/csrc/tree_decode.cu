@@ -36,9 +36,13 @@
 // per cell.  A pruned element thus takes no part whatever it holds.
 //
 // Precision.  q~ is kept as two bf16 parts (hi + lo, 2^-16 of its value), so
-// scores carry fp32-grade error; P is rounded to bf16 (the MMA's operand type,
-// V's own), which moves an output by at most 2^-8 of sum p |v|; sums, maxima and
-// O are fp32.
+// scores carry fp32-grade error; sums, maxima and O are fp32.  So is P (two parts, two
+// MMAs for each 16 keys) for fp32 outputs and for sequences with rows that may see 128
+// keys or fewer, where a rounding of P does not average out.  Otherwise P is rounded to
+// bf16 once, which moves an output by at most 2^-8 of sum p |v|, as much as its own
+// rounding to bf16 may.  (Two parts everywhere: tree_batch of the measured cases 63.6
+// us against 60.5, tree_single 116 against 108, tree_wide 430 against 368, and no
+// smaller error once the output is bf16: 4.8e-4 against 5.0e-4 on tree_batch.)
 //
 // Warps: the softmax warps, then one each for loading K, issuing QK, the fix-up of K
 // (boundary pairs staged, they and pruned pairs zeroed), issuing PV, loading V and
@@ -59,6 +63,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "serving.h"
@@ -80,6 +85,7 @@ constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles toget
 constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences when they took 71)
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
+constexpr int kShort = 128;      // a row that sees so few keys is one of a sequence with as few committed tokens
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 template <int D, bool kPacked>
@@ -103,8 +109,9 @@ struct Cfg {
     static constexpr int CtlBytes = 6144;
     static constexpr int Request = OffCtl + CtlBytes + 1024;
     static_assert(Request <= 232448, "shared memory of one CTA");
-    // TMEM: S of a tile in one of three buffers at 0, 128 and 256, its P (64 columns of bf16 pairs)
-    // over the columns of S that have been read, O at 384.
+    // TMEM: S of a tile in one of three buffers at 0, 128 and 256, its P over the columns of S that
+    // have been read (64 columns of bf16 pairs; in two parts, for each 16 keys 8 columns of high and 8
+    // of low parts in the place of their scores), O at 384.
     static constexpr uint32_t TmemO = 384, TmemCols = 512;
 };
 
@@ -116,6 +123,7 @@ struct Segment {
     int tile0, ntile, tiles;
     int pmin, pmax;   // positions of the row tile's nodes
     int kmin;         // smallest position of a node (as a key)
+    int fine;         // P in two bf16 parts
 };
 
 struct Ctl {
@@ -468,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.row0 = (item % s.groups * sh.R + member) * kBM;
                 g.rows = min(kBM, s.nodes * sh.G - g.row0);
                 g.tiles = s.tiles;
+                g.fine = a.out_f32 || s.L <= kShort;
                 g.tile0 = min(v0, s.tiles);
                 g.ntile = min(v0 + nv, s.tiles) - g.tile0;
                 if (g.ntile == 0) g.rows = 0;  // nothing but the item's cost
@@ -757,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sVa = smem_u32(sV);
         uint32_t tails = 0;  // phase bit of v_ready per stage
         while (ok && runs.next(wc, ok)) {
-            const int L = runs.now().L, tile0 = runs.now().tile0, ntile = runs.now().ntile;
+            const int L = runs.now().L, tile0 = runs.now().tile0, ntile = runs.now().ntile, fine = runs.now().fine;
             runs.done(lane);
             for (int j = tile0; ok && j < tile0 + ntile; ++j, ++it) {
                 const int st = it % ST, buf = it % kBufs;
@@ -769,10 +778,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&ctl->p_full[buf], (it / kBufs) & 1, wc, 52))) break;
                 if (lane == 0) {
                     tc_fence_after();
+                    const uint32_t o = tmem + F::TmemO, p = tmem + buf * kBN;
+                    if (fine) {
 #pragma unroll 1
-                    for (int kk = 0; kk < kBN / 16; ++kk) {
-                        const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
-                        umma_bf16_ts(tmem + F::TmemO, tmem + buf * kBN + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < kBN / 16; ++kk) {
+                            const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
+                            umma_bf16_ts(o, p + kk * 16, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
+                            umma_bf16_ts(o, p + kk * 16 + 8, db, idesc, 1u);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < kBN / 16; ++kk) {
+                            const uint64_t db = smem_desc(sVa + st * F::TileBytes + kk * 2048, 16384, 1024, kSwizzle128B);
+                            umma_bf16_ts(o, p + kk * 8, db, idesc, (j > tile0 || kk > 0) ? 1u : 0u);
+                        }
                     }
                     umma_commit(&ctl->o_done[buf]);
                     umma_commit(&ctl->v_empty[st]);
@@ -799,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         while (ok && runs.next(wc, ok)) {
             const Segment &g = runs.now();
-            const int rows = g.rows, row0 = g.row0, b = g.b, L = g.L, tile0 = g.tile0, ntile = g.ntile;
+            const int rows = g.rows, row0 = g.row0, b = g.b, L = g.L, tile0 = g.tile0, ntile = g.ntile, fine = g.fine;
             const bool live = (q4 * 32) % kRows < rows;  // some row of this warp exists
             const bool valid = row < rows;
             const int tok = (row0 + (valid ? row : 0)) / sh.G;
@@ -989,11 +1008,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mr = m_new == -INFINITY ? 0.f : m_new;  // nothing seen so far
                 const float2 mneg = make_float2(-mr, -mr), sc2 = make_float2(scale_log2, scale_log2);
                 float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-                if (live) {
+                const auto weigh = [&](auto parts) {
+                    constexpr bool kFine = decltype(parts)::value;
 #pragma unroll 1
                     for (int c = c0; c < c0 + NC; c += CW) {
                         if (NC > CW) load(c);
-                        uint32_t pk[CW / 2];
+                        uint32_t pk[kFine ? CW : CW / 2];  // two parts: of each 16 keys 8 high words, then 8 low ones
 #pragma unroll
                         for (int i = 0; i < CW / 2; i += 2) {
                             float2 xa = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mneg);
@@ -1004,20 +1024,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                             xb.y = fast_exp2(xb.y);
                             l0 = add2(l0, xa);
                             l1 = add2(l1, xb);
-                            pk[i] = pack_bf16x2(xa.x, xa.y);
-                            pk[i + 1] = pack_bf16x2(xb.x, xb.y);
+                            uint32_t *p = pk + (kFine ? i / 8 * 16 + i % 8 : i);
+                            p[0] = pack_bf16x2(xa.x, xa.y);
+                            p[1] = pack_bf16x2(xb.x, xb.y);
+                            if constexpr (kFine) {
+                                const float2 minus = make_float2(-1.f, -1.f);
+                                xa = fma2(make_float2(bf16lo(p[0]), bf16hi(p[0])), minus, xa);
+                                xb = fma2(make_float2(bf16lo(p[1]), bf16hi(p[1])), minus, xb);
+                                p[8] = pack_bf16x2(xa.x, xa.y);
+                                p[9] = pack_bf16x2(xb.x, xb.y);
+                            }
                         }
-                        tmem_st_x16(tS + c / 2, pk);
+                        if constexpr (kFine) tmem_st_32x32b_x32(tS + c, pk);
+                        else tmem_st_x16(tS + c / 2, pk);
                     }
                     if (kRep > 1) {
                         // P is zero in the other copies' columns.
-                        uint32_t zero[16];
+                        constexpr int kW = kFine ? 32 : 16;  // columns of 32 keys
+                        uint32_t zero[kW];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) zero[i] = 0;
+                        for (int i = 0; i < kW; ++i) zero[i] = 0;
 #pragma unroll 1
-                        for (int c = 0; c < kBN / 2; c += 16)
-                            if (c / (NC / 2) != copy) tmem_st_x16(tS + c, zero);
+                        for (int c = 0; c < kBN / 32; ++c) {
+                            if (c / (NC / 32) == copy) continue;
+                            if constexpr (kFine) tmem_st_32x32b_x32(tS + c * kW, zero);
+                            else tmem_st_x16(tS + c * kW, zero);
+                        }
                     }
+                };
+                if (live) {
+                    if (fine) weigh(std::true_type{});
+                    else weigh(std::false_type{});
                     const float2 ls = add2(l0, l1);
                     lrun += ls.x + ls.y;
                 }

@@ -89,11 +89,11 @@ def windows(theta, k):
     return [math.inf if math.isinf(k) else math.floor(k * 2 * math.pi / t) for t in theta]
 
 
-def tree(q, cache, lens, counts, positions, mask, theta, k):
+def tree(q, cache, lens, counts, positions, mask, theta, k, p_err=2.0 ** -8):
     """fp64 (out [B, T, Hq, D], lse [B, Hq, T], err [B, T, Hq, 1], lse_err [B, Hq, T]); rows past counts are NaN.
 
     err: what bf16 probabilities (2^-8 of each), the rotated query kept to 2^-16 and fp32 sums can move an output
-    by: (2^-8 + 2 e) * sum p |v| (largest over dims), with e = 2^-15 * max over keys of sum_r |terms| / sqrt(D) the
+    by: (2^-8 (or p_err) + 2 e) * sum p |v| (largest over dims), with e = 2^-15 * max over keys of sum_r |terms| / sqrt(D) the
     error of a score (2^-16 for the query's two bf16 parts, 2^-16 for a 256-term fp32 sum).  lse_err: e plus fp32
     roundings of the log (2^-20 of its size and one)."""
     B, T, Hq, D = q.shape
@@ -137,7 +137,7 @@ def tree(q, cache, lens, counts, positions, mask, theta, k):
             part = torch.stack([torch.where(sees[i][:, None], vh, 0.0).T @ p[i].T for i in range(t)]).transpose(1, 2)  # [t, G, D]
             mag = torch.stack([torch.where(sees[i][:, None], vh.abs(), 0.0).T @ p[i].T for i in range(t)]).transpose(1, 2)
             out[b, :t, h * G:(h + 1) * G] = part
-            err[b, :t, h * G:(h + 1) * G, 0] = (2.0 ** -8 + 2 * e) * mag.amax(-1)
+            err[b, :t, h * G:(h + 1) * G, 0] = (p_err + 2 * e) * mag.amax(-1)
             ls = torch.where(l[..., 0] == 0, -math.inf, m[..., 0] + torch.log(l[..., 0]))
             lse[b, h * G:(h + 1) * G, :t] = ls.T
             lse_err[b, h * G:(h + 1) * G, :t] = (e + 2.0 ** -20 * (1 + ls.nan_to_num(0, 0, 0).abs())).T

@@ -733,3 +733,61 @@ def test_copying_no_pages_changes_nothing(packed):
         a = {**dict(src=none, dst=none, tokens=None), **bad}
         with pytest.raises((ValueError, TypeError)):
             atf.cache_copy_pages(c.kpages, c.vpages, a["src"], a["dst"], 64, tokens=a["tokens"], kv_layout=c.layout)
+
+
+def fine_err(keys):
+    """What probabilities in two bf16 parts (2^-16 of each) and sums that may truncate move an output by, relative to
+    sum p |v|: two products and additions of at most 2^-23 for each key."""
+    return 2.0 ** -16 + 2 * keys * 2.0 ** -23
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv,lens,T,kind,dt", [
+    (64, 4, 2, [3, 60, 0, 120], 7, "tree", torch.bfloat16),     # rows of 1 to 127 keys, repeated in four copies
+    (128, 8, 1, [128, 1, 17], 8, "chain", torch.bfloat16),      # two copies; a row of 129 keys
+    (128, 12, 1, [40, 128], 30, "tree", torch.bfloat16),        # three row tiles; a second key tile
+    (64, 6, 1, [0, 50], 12, "any", torch.float32),
+    (128, 4, 2, [300, 10], 5, "tree", torch.float32),           # fp32 output: longer rows too
+    (64, 14, 2, [257, 190], 20, "tree", torch.float32),
+    (64, 2, 1, [500], 1, "chain", torch.float32),
+])
+def test_tree_of_few_keys_or_fp32_output_keeps_its_probabilities(packed, D, Hq, Hkv, lens, T, kind, dt):
+    # Small scores (their error stays far below a bf16 rounding of P) over values of both signs.
+    B, page, base, k, seed = len(lens), 64, 1e4, 8.0, 461
+    c = R.Cache(B, -(-(max(lens) + T) // page), page, Hkv, D, packed, seed)
+    for b in range(B):
+        n = lens[b] + T
+        c.write(b, torch.arange(n, device="cuda"), randn((n, Hkv, D), seed + 10 + b), randn((n, Hkv, D), seed + 20 + b))
+    q = (randn((B, T, Hq, D), seed + 1, torch.float32) / 8).to(torch.bfloat16)
+    rows = torch.arange(T, device="cuda", dtype=torch.int32)
+    mask, pos = torch.ones((B, T, T), dtype=torch.bool, device="cuda").tril(), ints(lens)[:, None] + rows
+    if kind == "tree":
+        mask, depth = R.random_tree(B, T, seed + 2)
+        pos = ints(lens)[:, None] + depth
+    elif kind == "any":
+        mask = (torch.rand((B, T, T), generator=torch.Generator().manual_seed(seed + 3)) < 0.4).cuda()
+    out, lse = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints(lens), page, base, k, tree_mask=mask, positions=pos,
+                                     kv_layout=c.layout, out_dtype=dt, return_lse=True)
+    ref, rlse, err, lerr = R.tree(q, c, lens, [T] * B, pos, mask, R.theta_of(base, D), k, p_err=fine_err(max(lens) + T))
+    R.close(out, ref, err.expand_as(ref) + ref.abs() * (HALF[dt] + 2.0 ** -21) + 1e-30, "out")
+    R.close(lse, rlse, lerr, "lse")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 2), (128, 8, 1)])
+def test_tree_of_one_token_is_the_decode_for_short_sequences(packed, D, Hq, Hkv):
+    # The decode computes sequences of up to 128 tokens in fp32.  (Scores here are small: queries of 1/8.)
+    lens, page, base, k = [1, 2, 9, 33, 64, 65, 127, 128], 64, 1e6, 16.0
+    c = R.Cache(len(lens), 2, page, Hkv, D, packed, 471)
+    for b, n in enumerate(lens):
+        c.write(b, torch.arange(n, device="cuda"), randn((n, Hkv, D), 472 + b), randn((n, Hkv, D), 492 + b))
+    q = (randn((len(lens), Hq, D), 512, torch.float32) / 8).to(torch.bfloat16)
+    want = atf.decode_paged(q, c.kpages, c.vpages, c.block_table, ints(lens), page, base, k, kcache_rotated=True, kv_layout=c.layout,
+                            out_dtype=torch.float32)
+    before = ints([n - 1 for n in lens])
+    ones = torch.ones((len(lens), 1, 1), dtype=torch.bool, device="cuda")
+    ref, _, err, _ = R.tree(q[:, None], c, before, [1] * len(lens), before[:, None], ones, R.theta_of(base, D), k, p_err=fine_err(128))
+    for dt in (torch.float32, torch.bfloat16):
+        got = atf.tree_decode_paged(q[:, None], c.kpages, c.vpages, c.block_table, before, page, base, k, kv_layout=c.layout, out_dtype=dt)
+        # Both are within err of the definition.
+        R.close(got[:, 0], want.double(), 2 * err[:, 0].expand_as(want) + want.abs() * (HALF[dt] + 2.0 ** -20), "one token")
