@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.row0 = (item % s.groups * sh.R + member) * kBM;
                 g.rows = min(kBM, s.nodes * sh.G - g.row0);
                 g.tiles = s.tiles;
-                g.fine = a.out_f32 || s.L <= kShort;
+                // A row sees its committed tokens, and in a chain the nodes up to its own.
+                g.fine = a.out_f32 || (a.mask ? s.L : s.L + g.row0 / sh.G + 1) <= kShort;
                 g.tile0 = min(v0, s.tiles);
                 g.ntile = min(v0 + nv, s.tiles) - g.tile0;
                 if (g.ntile == 0) g.rows = 0;  // nothing but the item's cost

@@ -791,3 +791,22 @@ def test_tree_of_one_token_is_the_decode_for_short_sequences(packed, D, Hq, Hkv)
         got = atf.tree_decode_paged(q[:, None], c.kpages, c.vpages, c.block_table, before, page, base, k, kv_layout=c.layout, out_dtype=dt)
         # Both are within err of the definition.
         R.close(got[:, 0], want.double(), 2 * err[:, 0].expand_as(want) + want.abs() * (HALF[dt] + 2.0 ** -20), "one token")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_tree_of_a_long_chain_keeps_the_probabilities_of_its_short_rows(packed):
+    # A prompt chunk of 300 tokens behind 20: rows of up to 128 keys end inside the first and the second row tile.
+    D, Hq, Hkv, page, T, L, base, k = 64, 2, 2, 64, 300, 20, 1e4, 8.0
+    for heads in (1, 2):  # query heads of one KV head: nodes 0..127 and 0..63 in the first tile
+        kv = Hq // heads
+        c = R.Cache(1, 6, page, kv, D, packed, 521)
+        c.write(0, torch.arange(L + T, device="cuda"), randn((L + T, kv, D), 522), randn((L + T, kv, D), 523))
+        q = (randn((1, T, Hq, D), 524, torch.float32) / 8).to(torch.bfloat16)
+        out = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints([L]), page, base, k, kv_layout=c.layout)
+        pos = L + torch.arange(T, device="cuda", dtype=torch.int32)[None]
+        mask = torch.ones((1, T, T), dtype=torch.bool, device="cuda").tril()
+        th, short = R.theta_of(base, D), 128 - L
+        ref, _, err, _ = R.tree(q[:, :short], c, [L], [short], pos[:, :short], mask[:, :short, :short], th, k, p_err=fine_err(128))
+        R.close(out[:, :short], ref, err.expand_as(ref) + ref.abs() * (HALF[torch.bfloat16] + 2.0 ** -21), "short rows")
+        ref, _, err, _ = R.tree(q, c, [L], [T], pos, mask, th, k)
+        R.close(out, ref, err.expand_as(ref) + ref.abs() * HALF[torch.bfloat16], "all rows")
