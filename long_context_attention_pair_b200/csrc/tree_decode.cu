@@ -238,10 +238,16 @@ constexpr int kPairsPerStep = kPacked ? 8 : 16;
 // keeps; r >= r_full kept for every cell.  The MMA starts at the K-step of rs.
 // Flags: boundary pairs exist (the fix-up warp has work); some cells are added; the
 // softmax warps hold the K stage.
+//
+// With a boundary pair rs < r_full <= H: either all of them are staged and rs = r_lo, or
+// r_full - kStaged is rounded up to a K-step and kStaged is one.  In a tile with nodes r_lo
+// is 0, so rs < H there too: the MMA leaves no S unwritten that cells are added to or
+// hidden in.
 enum : int { kBandFix = 1, kBandCells = 2, kBandHold = 4 };
 template <int D, bool kPacked>
 __device__ __forceinline__ int4 make_band(int r_lo, int r_full, bool spread) {
     constexpr int kPer = kPairsPerStep<kPacked>, kStaged = Cfg<D, kPacked>::Staged;
+    static_assert(kStaged >= kPer, "a K-step's pairs fit the staging");
     const int rs = r_full - r_lo > kStaged ? (r_full - kStaged + kPer - 1) / kPer * kPer : r_lo;
     int flags = r_lo < r_full ? kBandFix : 0;
     if (r_lo < rs || (spread && r_lo < r_full)) flags |= kBandCells | (!kPacked || r_lo < rs ? kBandHold : 0);
@@ -885,29 +891,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int4 bd = ctl->band[x % 8];
                 const bool cells = bd.w & kBandCells;
-                bool dense = bd.y < H;  // S holds something
+                const bool dense = bd.y < H;  // S holds something (always where cells are added or hidden: see make_band)
                 if (tail) {
                     if (!(ok = wait(&ctl->m_full[set], tails & 1, wc, 58))) break;
                     ++tails;
                 }
                 if (cells || tail) {
                     // Cells added or hidden, in S itself, 32 columns at a time.
-                    const uint32_t chunks = (cells ? ctl->chunks[cb] : 0u) | (tail || !dense ? 0xfu : 0u);
+                    const uint32_t chunks = (cells ? ctl->chunks[cb] : 0u) | (tail ? 0xfu : 0u);
 #pragma unroll 1
                     for (int cc = c0; live && cc < c0 + NC; cc += 32) {
                         if (!((chunks >> (cc / 32)) & 1u)) continue;
                         uint32_t ra[32];
                         float s[32];
                         __syncwarp();
-                        if (dense) {
-                            tmem_ld_32x32b_x32(tS + cc, ra);
-                            tmem_ld_wait(ra);
+                        tmem_ld_32x32b_x32(tS + cc, ra);
+                        tmem_ld_wait(ra);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(ra[i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = 0.f;
-                        }
+                        for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(ra[i]);
                         if (cells) {
                             const int4 *kp = reinterpret_cast<const int4 *>(sKpos + cb * kBN + cc);
 #pragma unroll 1
@@ -956,7 +957,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st_32x32b_x32(tS + cc, ra);
                     }
                     tmem_st_wait();
-                    dense = true;
                     __syncwarp();
                     if ((bd.w & kBandHold) && lane == 0) mbar_arrive(&ctl->k_empty[st]);
                     if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
