@@ -810,3 +810,79 @@ def test_tree_of_a_long_chain_keeps_the_probabilities_of_its_short_rows(packed):
         R.close(out[:, :short], ref, err.expand_as(ref) + ref.abs() * (HALF[torch.bfloat16] + 2.0 ** -21), "short rows")
         ref, _, err, _ = R.tree(q, c, [L], [T], pos, mask, th, k)
         R.close(out, ref, err.expand_as(ref) + ref.abs() * HALF[torch.bfloat16], "all rows")
+
+
+def one_pair_key(q, pos, node, r, theta):
+    """A rotated key [1, D] whose pair r alone is not zero: along the rotated pair of q[node, 0], scaled to a score of 8."""
+    D = q.shape[-1]
+    x = R.rope(q[None, node:node + 1, :1], pos[None, node:node + 1], theta)[0, 0, 0]
+    a = torch.stack((x[r], x[r + D // 2]))
+    key = torch.zeros((1, D), dtype=torch.float64, device="cuda")
+    key[0, r], key[0, r + D // 2] = a * (8 * math.sqrt(D) / float((a * a).sum()))
+    return key.to(torch.bfloat16)
+
+
+# Windows of these tests run from one or a few positions to beyond the cache.
+BOUNDARY = [
+    # D, Hq, T, L, base, k: rows in four copies, two copies, one; prefixes that end inside a tile and with one
+    (64, 1, 12, 389, 1e4, 0.5),
+    (64, 4, 12, 384, 1e4, 0.5),
+    (128, 2, 12, 450, 1e4, 0.25),
+    (128, 8, 12, 512, 1e6, 0.25),   # more boundary pairs in a tile than are staged
+    (128, 1, 1, 500, 1e4, 0.25),    # a single token
+]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,T,L,base,k", BOUNDARY)
+def test_tree_windows_end_where_they_should_for_every_node(packed, D, Hq, T, L, base, k):
+    # A sequence for each pair r, node and side of its window: the one key that is not zero lies at distance w_r
+    # (kept) or w_r + 1 (not kept) of that node. Its pair moves the log-sum-exp by units where it is kept.
+    theta, page = R.theta_of(base, D), 64
+    mask, depth = R.random_tree(1, T, 531)
+    pos1 = L + depth[0]
+    order = torch.argsort(depth[0])
+    nodes = sorted({int(order[0]), int(order[T // 2]), int(order[-1])})
+    cases = [(r, i, int(pos1[i]) - int(w) - over) for r, w in enumerate(R.windows(theta, k)) for i in nodes for over in (0, 1)
+             if 0 <= int(pos1[i]) - int(w) - over < L]
+    B = len(cases)
+    q1 = randn((T, Hq, D), 532, torch.float32).mul_(4).to(torch.bfloat16)
+    c = R.Cache(B, -(-(L + T) // page), page, 1, D, packed, 533, fill=0.0)
+    c.vpages.copy_(randn(c.vpages.shape, 534))
+    for b, (r, i, slot) in enumerate(cases):
+        at = torch.tensor([slot], device="cuda")
+        c.write(b, at, one_pair_key(q1, pos1, i, r, theta)[:, None], c.read(b, at)[1])
+    q, pos = q1.expand(B, -1, -1, -1).contiguous(), pos1.expand(B, -1).contiguous()
+    m = mask.expand(B, -1, -1).contiguous()
+    out, lse = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints([L] * B), page, base, k, tree_mask=m, positions=pos,
+                                     kv_layout=c.layout, return_lse=True, out_dtype=torch.float32)
+    ref, rlse, err, lerr = R.tree(q, c, [L] * B, [T] * B, pos, m, theta, k)
+    for b, (r, i, slot) in enumerate(cases):  # the two sides differ by far more than the tolerance
+        if b % 2 and cases[b - 1][:2] == (r, i):
+            assert float((rlse[b - 1, 0, i] - rlse[b, 0, i]).abs()) > 100 * float(lerr[b, 0, i])
+    R.close(lse, rlse, lerr, "lse")
+    R.close(out, ref, err.expand_as(ref) + ref.abs() * 2.0 ** -24, "out")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,base,k,L", [(64, 1, 1e4, 0.5, 60), (64, 14, 1e4, 0.5, 128), (128, 4, 1e6, 0.25, 90)])
+def test_tree_windows_end_where_they_should_between_nodes(packed, D, Hq, base, k, L):
+    # Node 0's key has one pair; the other nodes sit at distances around its window, on both sides.
+    theta, page = R.theta_of(base, D), 64
+    steps = [0, -3, -1, 0, 1, 2, 40]
+    T, w = len(steps), R.windows(theta, k)
+    B = len(w)
+    pos = ints([[L + 7] + [max(0, L + 7 + int(x) + s) for s in steps[1:]] for x in w])
+    q = randn((1, T, Hq, D), 541, torch.float32).mul_(4).to(torch.bfloat16).expand(B, -1, -1, -1).contiguous()
+    c = R.Cache(B, -(-(L + T) // page), page, 1, D, packed, 542, fill=0.0)
+    c.vpages.copy_(randn(c.vpages.shape, 543))
+    at = torch.tensor([L], device="cuda")
+    for b in range(B):
+        c.write(b, at, one_pair_key(q[b], pos[b], 3, b, theta)[:, None], c.read(b, at)[1])
+    m = torch.ones((B, T, T), dtype=torch.bool, device="cuda")
+    out, lse = atf.tree_decode_paged(q, c.kpages, c.vpages, c.block_table, ints([L] * B), page, base, k, tree_mask=m, positions=pos,
+                                     kv_layout=c.layout, return_lse=True, out_dtype=torch.float32)
+    ref, rlse, err, lerr = R.tree(q, c, [L] * B, [T] * B, pos, m, theta, k)
+    assert bool(((rlse[:, 0, 3] - math.log(L + T)) > 100 * lerr[:, 0, 3]).all())  # kept at distance w_r
+    R.close(lse, rlse, lerr, "lse")
+    R.close(out, ref, err.expand_as(ref) + ref.abs() * 2.0 ** -24, "out")
