@@ -85,6 +85,7 @@ constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles toget
 constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences when they took 71)
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
+constexpr int kMergeThreads = 256;
 constexpr int kShort = 128;      // a row that sees so few keys is one of a sequence with as few committed tokens
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
@@ -177,14 +178,6 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, const Shape &sh, int b)
 __device__ __forceinline__ int item_units(const Seq &s) { return s.tiles ? s.tiles + kItemCost : 0; }
 __device__ __forceinline__ int64_t units_of(const Seq &s, int Hkv) { return (int64_t)Hkv * s.groups * item_units(s); }
 
-// Units before sequence `b` (all of them for b = B), by a whole warp.
-__device__ __forceinline__ int64_t units_before(const TreeArgs &a, const Shape &sh, int b) {
-    int64_t sum = 0;
-    for (int x = threadIdx.x & 31; x < b; x += 32) sum += units_of(seq_of(a, sh, x), sh.Hkv);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-}
 // CTA groups with work, and the first unit of group g.
 __device__ __forceinline__ int active_groups(int64_t total, int groups) { return total < groups ? (int)total : groups; }
 __device__ __forceinline__ int64_t first_unit(int64_t total, int active, int g) {
@@ -1217,40 +1210,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the partial states of the rows whose item was cut between CTA groups; a
-// warp takes one row.  Rows of whole items were written by the kernel above.
+// Joins the partial states of the items that were cut between CTA groups.  A block takes eight
+// rows of one row tile at one cut (the first unit of a group): at most 147 cuts, however
+// many rows the batch has.  The first cut of an item does the work for all of its cuts, in
+// the order of the groups; a warp takes one row.  Rows of whole items were written by the
+// kernel above.  (A warp for every row of the batch, each adding up the units before it:
+// 3.9 ms a call on 2048 sequences of 8 nodes and 32 heads, 1.1 now.  Two and four rows to a
+// warp, in turn: 26 and 30 us where one takes 23, on one sequence of 1021 tokens.)
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Shape sh) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Shape sh,
+                                                                   int row_blocks) {
     constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t id64 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const bool exists = id64 < (int64_t)a.B * a.T * a.Hq;
-    const int id = exists ? (int)id64 : 0;  // rows fit 31 bits
-    const int hq = id % a.Hq, i = id / a.Hq % a.T, b = id / a.Hq / a.T;
-    const Seq s = seq_of(a, sh, b);
-    const int64_t before = units_before(a, sh, b), total = units_before(a, sh, sh.B);
-    if (exists && i == 0 && hq == 0 && lane == 0) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int member = blockIdx.x / row_blocks % sh.R, g0 = blockIdx.x / row_blocks / sh.R;
+    const int row = blockIdx.x % row_blocks * (kMergeThreads / 32) + warp;
+    // Sequences that have no room for their nodes: reported here, a thread each.
+    for (int b = blockIdx.x * kMergeThreads + threadIdx.x; b < sh.B; b += gridDim.x * kMergeThreads) {
         const int64_t L = a.seqlens[b];
         const int n = a.counts ? max(0, min(a.counts[b], a.T)) : a.T;
         if (L < 0 || L + n > (int64_t)a.pk.max_pages * a.pk.page_size) atomicCAS(a.status, 0, ATFLASH_DEVICE_BAD_PAGE);
     }
-    pdl_wait();  // by every warp, so that this grid never ends before the one it depends on
-    if (!exists || i >= s.nodes) return;
-    const int h = hq / sh.G, r = i * sh.G + hq % sh.G, rt = r / kBM;
-    const int64_t first = before + ((int64_t)h * s.groups + rt / sh.R) * item_units(s);
+    // Units of this thread's sequences, before them, and of the batch.
+    __shared__ int64_t warp_units[kMergeThreads / 32], at_units;
+    __shared__ int at_b;
+    const int each = (sh.B - 1) / kMergeThreads + 1, b0 = min((int)threadIdx.x * each, sh.B), b1 = min(b0 + each, sh.B);
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) own += units_of(seq_of(a, sh, b), sh.Hkv);
+    int64_t before = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) warp_units[warp] = before;
+    __syncthreads();
+    before -= own;
+    int64_t total = 0;
+    for (int x = 0; x < kMergeThreads / 32; ++x) {
+        if (x < warp) before += warp_units[x];
+        total += warp_units[x];
+    }
+    // The sequence that holds the cut's unit.
     const int active = active_groups(total, sh.groups);
-    // Group of unit x: the largest g with floor(g * total / active) <= x.
-    const auto group_of = [&](int64_t x) {
-        const int64_t y = (x + 1) * active - 1;
-        return (int)((y | total) >> 31 ? y / total : (uint32_t)y / (uint32_t)total);
-    };
-    const int g0 = group_of(first), g1 = group_of(first + s.tiles - 1);
-    if (g0 == g1) return;
-    const int row = r % kBM;
+    const int64_t cut = g0 + 1 < active ? first_unit(total, active, g0 + 1) : -1;
+    if (cut >= before && cut < before + own) {
+        int b = b0;
+        for (int64_t n; cut >= before + (n = units_of(seq_of(a, sh, b), sh.Hkv)); ++b) before += n;
+        at_units = before;
+        at_b = b;
+    }
+    __syncthreads();
+    // Blocks without work end at once and make room; the first one waits in any case, so that this
+    // grid never ends before the one it depends on.
+    if (blockIdx.x == 0) pdl_wait();
+    if (cut < 0) return;
+    const int b = at_b;
+    const Seq s = seq_of(a, sh, b);
+    const int64_t off = cut - at_units;
+    const int per = item_units(s);
+    const int item = (int)(off >> 31 ? off / per : (uint32_t)off / (uint32_t)per);
+    const int64_t first = at_units + (int64_t)item * per;
+    // No cut between two items, nor in an item's cost; and the item's first cut only.
+    if (cut == first || cut - first >= s.tiles || first_unit(total, active, g0) > first) return;
+    const int row0 = (item % s.groups * sh.R + member) * kBM;
+    if (row >= s.nodes * sh.G - row0) return;
+    // Group of the last tile's unit x: the largest g with floor(g * total / active) <= x.
+    const int64_t y = (first + s.tiles) * active - 1;
+    const int g1 = (int)((y | total) >> 31 ? y / total : (uint32_t)y / (uint32_t)total);
     auto state = [&](int g) {
         // The item is the last of group g0's run and the first of the later ones'.
-        return a.workspace + (((size_t)g * sh.R + rt % sh.R) * 2 + (g == g0 ? 1 : 0)) * kBM * (D + 2);
+        return a.workspace + (((size_t)g * sh.R + member) * 2 + (g == g0 ? 1 : 0)) * kBM * (D + 2);
     };
+    pdl_wait();
     float M = -INFINITY;
     for (int g = g0 + lane; g <= g1; g += 32) M = fmaxf(M, state(g)[row]);
 #pragma unroll
@@ -1269,11 +1300,12 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
         for (int v = 0; v < V; ++v) acc[v] += o[v] * f;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t off = (size_t)id * D + lane * V;
+    const int i = (row0 + row) / sh.G, hq = item / s.groups * sh.G + (row0 + row) % sh.G;
+    const size_t to = (((size_t)b * a.T + i) * a.Hq + hq) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (a.out_f32) static_cast<float *>(a.out)[off + v] = acc[v] * inv;
-        else static_cast<__nv_bfloat16 *>(a.out)[off + v] = __float2bfloat16_rn(acc[v] * inv);
+        if (a.out_f32) static_cast<float *>(a.out)[to + v] = acc[v] * inv;
+        else static_cast<__nv_bfloat16 *>(a.out)[to + v] = __float2bfloat16_rn(acc[v] * inv);
     }
     if (a.lse && lane == 0)
         a.lse[((size_t)b * a.Hq + hq) * a.T + i] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
@@ -1332,8 +1364,14 @@ cudaError_t launch(const TreeArgs &a, const WindowParams &wp, const RopeTurns &r
     }
     tree_decode_kernel<D, kPacked, NC><<<sh.groups * sh.R, kThreads, Cfg<D, kPacked>::Request, s>>>(tk, tv, a, sh, wp, rt, box_keys);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.B * a.T * a.Hq;
-    return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a, sh);
+    // As many cuts as CTA groups that can have work (units of the longest sequences that the table
+    // has room for), less one; of a single row tile, the rows that exist.
+    const int64_t rows = (int64_t)a.T * sh.G, row_groups = (rows + kBM * sh.R - 1) / (kBM * sh.R);
+    const int64_t tiles = ((int64_t)a.pk.max_pages * a.pk.page_size + kBN - 1) / kBN;
+    const int64_t units = a.B * row_groups * a.Hkv * (tiles + kItemCost);
+    const int cuts = (int)(units < sh.groups ? units : sh.groups) - 1;
+    const int row_blocks = (int)((rows < kBM ? rows : kBM) + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+    return launch_dependent(tree_merge_kernel<D>, dim3((unsigned)(cuts * sh.R * row_blocks)), dim3(kMergeThreads), 0, s, a, sh, row_blocks);
 }
 
 }  // namespace tree

@@ -886,3 +886,12 @@ def test_tree_windows_end_where_they_should_between_nodes(packed, D, Hq, base, k
     assert bool(((rlse[:, 0, 3] - math.log(L + T)) > 100 * lerr[:, 0, 3]).all())  # kept at distance w_r
     R.close(lse, rlse, lerr, "lse")
     R.close(out, ref, err.expand_as(ref) + ref.abs() * 2.0 ** -24, "out")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv,B,T", [(64, 2, 1, 700, 3), (128, 8, 1, 300, 17)])
+def test_tree_of_more_sequences_than_a_block_has_threads(packed, D, Hq, Hkv, B, T):
+    # A few items for each CTA group, most cuts inside an item, some at its ends; sequences without nodes, and (second
+    # case) two row tiles of which small trees have one.
+    lens = [(i * 173) % 611 for i in range(B)]
+    run_tree(D, Hq, Hkv, 64, packed, lens, T, [(i * 7) % (T + 3) - 1 for i in range(B)], "tree", 2.0, seed=551)
