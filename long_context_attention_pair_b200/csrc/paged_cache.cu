@@ -195,8 +195,7 @@ cudaError_t launch_cache_append(const AppendArgs &a, const RopeTurns &rt, cudaSt
     const int64_t blocks = ((int64_t)a.B * a.T * (a.D / 16) + 255) / 256;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     constexpr int smem = kStages * 4 * 256 * 16;
-    cudaError_t e = cudaFuncSetAttribute(cache_append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static_assert(smem + 64 * 8 <= 48 * 1024, "the ring and the turn counts need no opt-in");
     cache_append_kernel<<<(unsigned)blocks, 256, smem, s>>>(a, rt);
     return cudaGetLastError();
 }
