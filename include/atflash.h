@@ -381,7 +381,8 @@ int atflash_decode_paged_theta(const void *q, const void *kpages, const void *vp
  *   inverse     1: angles negated.  With the same scale this is the gradient of
  *               the call with inverse == 0.
  *   dtype       ATFLASH_BF16 or ATFLASH_F32; arithmetic in fp32, angles reduced
- *               exactly, one rounding at the end.
+ *               exactly: an element of a pair (x, z) is within scale * 2^-20
+ *               (|x| + |z|) before its one rounding at the end.
  *   D even, 2..256; B*T <= 2^31 - 1; Hq, Hkv <= 32767; tensors 16-byte aligned.
  * The _theta form takes R/2 frequencies (HOST, as described for the scaled-RoPE
  * calls above).

@@ -559,7 +559,9 @@ def rope_apply(q, k, positions, rope_base: float, *, rotary_dim=None, interleave
     cos and sin multiplied by ``scale``; the rest is copied.  ``inverse`` negates the
     angles: the gradient of the same call without it.  ``out_q=q, out_k=k`` works in
     place.  ``theta`` (R/2 frequencies) replaces base^(-2r/R).  Returns (q, k) rotated,
-    or the rotated q alone when k is None.
+    or the rotated q alone when k is None.  As all calls here, it is not recorded by
+    autograd: the results have no ``grad_fn``, and a training step calls it with
+    ``inverse`` on the gradients (in a ``torch.autograd.Function``, say).
     """
     torch = _torch()
     B, T, Hq, D = q.shape

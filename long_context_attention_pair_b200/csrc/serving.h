@@ -31,8 +31,10 @@ __device__ __forceinline__ float2 turn_cos_sin(int32_t pos, uint64_t turn) {
     return make_float2(c, s);
 }
 
-// The same by the hardware's sin and cos, within 2^-21 on [-pi, pi]: for results rounded
-// to bf16 (2^-8 of their value).
+// The same by the hardware's sin and cos (2^-21.2 on [-pi, pi]) of the angle in radians
+// (three roundings, 3 * 2^-23): a rotated element x c - z s is within 2^-20 (|x| + |z|),
+// products included.  For results rounded to bf16, half a step of which is 2^-8 of the
+// result: the bound is larger only where the two products cancel to 2^-12 of their sizes.
 __device__ __forceinline__ float2 turn_cos_sin_fast(int32_t pos, uint64_t turn) {
     float s, c;
     __sincosf((float)(int64_t)((uint64_t)(int64_t)pos * turn) * 3.4061215800865545e-19f, &s, &c);  // 2 pi / 2^64

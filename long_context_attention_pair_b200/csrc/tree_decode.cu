@@ -15,10 +15,12 @@
 // tiles); R CTAs, one for each row tile of the group, walk the same units at the
 // same time (the second reads of a tile hit L2).  The units of the whole batch,
 // counted on the device from seqlens and counts, are cut into equal runs, one for
-// each of the 148 / R CTA groups, so a ragged batch loads the SMs evenly and no
-// length is known on the host.  A run that covers an item whole writes its output;
-// otherwise it leaves (max, sum, unscaled output) in the workspace, at most twice
-// per CTA (its first and its last item), and tree_merge_kernel joins them.
+// each of the 148 / R CTA groups, so sequences of unequal lengths load the groups
+// evenly and no length is known on the host.  (Unequal node counts do not where R > 1:
+// R comes from T, and CTAs whose row tiles a smaller tree lacks skip its items.)  A run
+// that covers an item whole writes its output; otherwise it leaves (max, sum, unscaled
+// output) in the workspace, at most twice per CTA (its first and its last item), and
+// tree_merge_kernel joins them.
 //
 // Softmax.  Two sets of four warps take alternate key tiles; a row's two warps hand
 // its running max on from tile to tile and add into one O, so a set has two tile
@@ -40,9 +42,10 @@
 // MMAs for each 16 keys) for fp32 outputs and for sequences with rows that may see 128
 // keys or fewer, where a rounding of P does not average out.  Otherwise P is rounded to
 // bf16 once, which moves an output by at most 2^-8 of sum p |v|, as much as its own
-// rounding to bf16 may.  (Two parts everywhere: tree_batch of the measured cases 63.6
-// us against 60.5, tree_single 116 against 108, tree_wide 430 against 368, and no
-// smaller error once the output is bf16: 4.8e-4 against 5.0e-4 on tree_batch.)
+// rounding to bf16 may.  On 8 ragged sequences of up to 8192 keys the rms error of bf16
+// outputs is 0.0023 of theirs (0.0017 with two parts, their own rounding), of fp32 ones
+// 4e-6.  Two parts everywhere took 63.6 us against 60.5 there, 116 against 108 on 4
+// sequences of 64K keys and 430 against 368 on 2 of 128K with trees of 64 nodes.
 //
 // Warps: the softmax warps, then one each for loading K, issuing QK, the fix-up of K
 // (boundary pairs staged, they and pruned pairs zeroed), issuing PV, loading V and
@@ -51,14 +54,19 @@
 // bounded; on expiry the CTA records ATFLASH_ERR_TIMEOUT, lets its copies and MMAs finish
 // and exits.
 //
-// What bounds it.  A key tile takes 2 200 to 2 600 clocks: two K stages (D = 128) whose
-// cycle is copy issue 900, arrival 1 300 to 1 900, fix-up 400, QK 1 200 to 1 600 and
-// release 300.  Ten roles share the instruction caches, so short loops beat unrolled ones
-// everywhere (the MMA issue loops: 68 -> 61 us on 8 ragged sequences of up to 8192 keys
-// with trees of 16).  A CTA's first P comes about 20 000 clocks after its start, through
-// code that is fetched cold, which bounds small calls (24 us).  4 sequences of 64K keys,
-// one token each, no window: 106 us, 0.77 of the copy rate; 2 of 128K keys with trees of
-// 64 nodes (448 rows per KV head): 340 us, 570 TFLOP/s without the second part of q~.
+// What bounds it.  A steady key tile takes 2 200 to 2 600 clocks: two K stages (D = 128)
+// whose cycle is copy issue 900, arrival 1 300 to 1 900, fix-up 400, QK 1 200 to 1 600 and
+// release 300.  Within it the tensor pipe has 1 190 clocks of work on 2 sequences of 128K
+// keys with trees of 64 nodes and k = 16 (5.3 of 8 K-steps of QK, each for both parts of
+// q~, and PV: 320 GFLOP issued, padded rows included, where the kept pairs and one part of
+// q~ need 194) and the exponentials 1 024; its counters read 44 % (tensor) and 56 % (tc) of
+// the elapsed clocks.  A CTA's first P comes about 20 000 clocks after its start, through
+// code that is fetched cold, and a change of item costs as much again: that bounds small
+// calls and ragged batches, and there short loops beat unrolled ones (the MMA issue loops:
+// 68 -> 61 us on 8 ragged sequences of up to 8192 keys with trees of 16).  Device time back
+// to back in bursts at 1965 MHz: 1 sequence of 1021 keys 22.4 us; the 8 ragged ones 60.9;
+// 4 sequences of 64K keys, one token each, no window 106, 0.77 of the copy rate; the 2 of
+// 128K keys 342, 566 TFLOP/s of the 194 GFLOP.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -82,7 +90,11 @@ constexpr int kLaunchRegs = 128, kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kSMs = 148;
 constexpr int kMaxGroup = 8;     // row tiles that walk the same key tiles together
-constexpr int kItemCost = 6;         // key tiles that an item's own cost counts for (0, 3, 6, 10 measured 82, 73, 71, 75 us on 8 ragged sequences when they took 71)
+// Key tiles that an item's own cost counts for.  us for 3, 6, 8, 10, 12: 8 ragged sequences of
+// up to 8192 keys (48 rows) 61.7, 60.8, 62.4, 64.2, 64.2; 32 of up to 4000 111, 98.9, 101, 102,
+// 104; 6 of up to 16K with 448 rows 134, 125, 124, 123, 124; 6 of up to 30K with 14 rows 63.9,
+// 64.3, 64.9, 64.3, 65.5.
+constexpr int kItemCost = 6;
 constexpr int kBufs = 3;         // S / P buffers
 constexpr int kRing = 4;         // runs of tiles published ahead
 constexpr int kMergeThreads = 256;
@@ -854,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t wa = i < 2 ? ya.x : ya.y, wb = i < 2 ? yb.x : yb.y;
                         const float fa = i & 1 ? bf16hi(wa) : bf16lo(wa), fb = i & 1 ? bf16hi(wb) : bf16lo(wb);
-                        // The hardware's sin and cos (2^-21 on [-pi, pi]) lie far below the 2^-16 of hi + lo.
+                        // (Within 2^-20 (|fa| + |fb|), far below the 2^-16 of hi + lo.)
                         const float2 cs = turn_cos_sin_fast(pos, turn[i]);
                         const float x = fa * cs.x - fb * cs.y, y = fb * cs.x + fa * cs.y;
                         hi[i] = pack_bf16x2(x, y);
@@ -955,8 +967,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tail && lane == 0) mbar_arrive(&ctl->m_empty[set]);
                 }
                 // The row's maximum, then the exponentials, CW columns at a time.  More columns are read
-                // twice, by loops: their unrolled code would not stay in the instruction cache (on 8
-                // sequences of 512 nodes: 128 columns unrolled 498 us, 64 at a time 439, 32 384; 16 354 to 32's 343 later).
+                // twice, by loops: their unrolled code would not stay in the instruction cache (on 2
+                // sequences of 128K keys with trees of 64 nodes: 128 columns unrolled 498 us, 64 at a time 439, 32 384;
+                // later 16 took 354 and 32 343).
                 float s[CW], row_max = -INFINITY;
                 auto load = [&](int c) {
                     if (dense) {
