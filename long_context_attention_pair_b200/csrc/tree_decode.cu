@@ -926,19 +926,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t ql = load_pair<D, kPacked>(sQ + F::TileBytes, copy * kRows + row, r);
                                 const float qa = bf16lo(qh) + bf16lo(ql), qb = bf16hi(qh) + bf16hi(ql);
                                 // This row keeps keys at positions >= lim; of a staged pair the MMA has
-                                // those at lim + span and beyond (differences modulo 2^32 are exact here).
+                                // those at lim + span and beyond (differences modulo 2^32 are exact here,
+                                // and taken in unsigned arithmetic: they pass 31 bits).
                                 const int lim = pos - w[r];
                                 if (r >= bd.y) {
-                                    const uint32_t span = (uint32_t)(pmax - pos);
+                                    const uint32_t span = (uint32_t)(pmax - pos), low = (uint32_t)lim;
                                     const uint4 *kw = reinterpret_cast<const uint4 *>(sStage + (cb * kStaged + r - bd.y) * kBN + cc);
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) {
                                         const uint4 k = kw[i];
                                         const int4 p = kp[i];
-                                        s[4 * i] += (uint32_t)(p.x - lim) < span ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
-                                        s[4 * i + 1] += (uint32_t)(p.y - lim) < span ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
-                                        s[4 * i + 2] += (uint32_t)(p.z - lim) < span ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
-                                        s[4 * i + 3] += (uint32_t)(p.w - lim) < span ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
+                                        s[4 * i] += (uint32_t)p.x - low < span ? fmaf(qa, bf16lo(k.x), qb * bf16hi(k.x)) : 0.f;
+                                        s[4 * i + 1] += (uint32_t)p.y - low < span ? fmaf(qa, bf16lo(k.y), qb * bf16hi(k.y)) : 0.f;
+                                        s[4 * i + 2] += (uint32_t)p.z - low < span ? fmaf(qa, bf16lo(k.z), qb * bf16hi(k.z)) : 0.f;
+                                        s[4 * i + 3] += (uint32_t)p.w - low < span ? fmaf(qa, bf16lo(k.w), qb * bf16hi(k.w)) : 0.f;
                                     }
                                 } else {
                                     const uint8_t *kst = sK + st * F::TileBytes;
