@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) decode_tc_kernel(
             __syncwarp();
             last[st] = it;
         }
-        if (!ok && lane == 0) {
+        if (lane == 0) {
+            // Let every copy land before the CTA exits, also after the last stage: a consumer's wait may
+            // run out before anyone has waited for it.
             for (int s = 0; s < kStages; ++s) {
                 if (last[s] < 0) continue;
                 const uint64_t t0 = globaltimer_ns();

@@ -122,6 +122,7 @@ struct Ctl {
     uint64_t xbar[2][4];             // (head, lane quarter): both column halves have posted
     uint32_t tmem_base;
     int abort_flag;
+    int issued_k, issued_v;  // tiles whose copies the producer has started, once it has left its loop
     int w[kMaxPairs];
     float xval[2][4][2][2][32];      // (head, quarter, tile parity, column half, lane)
 };
@@ -309,45 +310,35 @@ __global__ void __launch_bounds__(Warps<NH, CH>::Threads, 3 - NH)
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
-            int last_k[KS], last_v[VS];
-            for (int s = 0; s < KS; ++s) last_k[s] = -1;
-            for (int s = 0; s < VS; ++s) last_v[s] = -1;
             mbar_expect_tx(&ctl->q_full, (uint32_t)(nwg * F::QBytes));
             for (int t = 0; t < nwg; ++t)
                 for (int c = 0; c < C; ++c)
                     tma_load_3d(sQ + t * F::QBytes + c * kChunkBytes, &tm_q, &ctl->q_full, 0, (int)(tokbase + n0),
                                 (bz * Hq + h0 + t) * C + c);
-            bool ok = true;
             BandWalk bw;
             bw.init(w, H, n0);
-            for (int it = 0, j = tiles.first(); j < nkt && ok; ++it, j = tiles.after(j)) {
+            int issued_k = 0, issued_v = 0;  // tiles whose copies have been started
+            for (int it = 0, j = tiles.first(); j < nkt; ++it, j = tiles.after(j)) {
                 const int ks = it % KS, vs = it % VS;
                 const int64_t m0 = (int64_t)j * kBN;
                 const int ca = bw.at(w, n0, m0).r_lo >> 3;
                 wc.site = 1;
-                if (!(ok = mbar_wait(&ctl->k_empty[ks], ((it / KS) & 1) ^ 1, wc))) break;
+                if (!mbar_wait(&ctl->k_empty[ks], ((it / KS) & 1) ^ 1, wc)) break;
                 mbar_expect_tx(&ctl->k_full[ks], (uint32_t)(C - ca) * kChunkBytes);
                 for (int c = ca; c < C; ++c)
                     tma_load_3d(sK + ks * F::KBytes + c * kChunkBytes, &tm_k, &ctl->k_full[ks], 0,
                                 (int)(tokbase + m0), (bz * Hkv + kvh) * C + c);
-                last_k[ks] = it;
+                issued_k = it + 1;
                 wc.site = 2;
-                if (!(ok = mbar_wait(&ctl->v_empty[vs], ((it / VS) & 1) ^ 1, wc))) break;
+                if (!mbar_wait(&ctl->v_empty[vs], ((it / VS) & 1) ^ 1, wc)) break;
                 mbar_expect_tx(&ctl->v_full[vs], F::VBytes);
                 for (int gidx = 0; gidx < D / 64; ++gidx)
                     tma_load_4d(sV + vs * F::VBytes + gidx * 16384, &tm_v, &ctl->v_full[vs], gidx * 64, kvh,
                                 (int)(tokbase + m0), bz);
-                last_v[vs] = it;
+                issued_v = it + 1;
             }
-            if (!ok) {
-                // Let every copy this thread started land before the CTA exits.
-                const uint64_t drain_ns = atflash_drain_limit_ns(limit_ns);
-                wait_drain(&ctl->q_full, 0, drain_ns);
-                for (int s = 0; s < KS; ++s)
-                    if (last_k[s] >= 0) wait_drain(&ctl->k_full[s], (last_k[s] / KS) & 1, drain_ns);
-                for (int s = 0; s < VS; ++s)
-                    if (last_v[s] >= 0) wait_drain(&ctl->v_full[s], (last_v[s] / VS) & 1, drain_ns);
-            }
+            ctl->issued_k = issued_k;  // for the teardown
+            ctl->issued_v = issued_v;
         }
     } else if (warp == kWarpFix) {
         // ------------------------- pruned-pair zeroing and boundary staging
@@ -736,6 +727,17 @@ __global__ void __launch_bounds__(Warps<NH, CH>::Threads, 3 - NH)
 
     // Teardown: every tensor-core operation must be complete before TMEM is freed.
     __syncthreads();
+    if (warp == kWarpProducer && lane == 0 && ctl->abort_flag) {
+        // A wait has run out, its own or another warp's after this thread's last copies: let every
+        // copy land before the CTA exits.  (Otherwise all have been waited for.)
+        const uint64_t drain_ns = atflash_drain_limit_ns(limit_ns);
+        const int issued_k = ctl->issued_k, issued_v = ctl->issued_v;
+        wait_drain(&ctl->q_full, 0, drain_ns);
+        for (int x = issued_k > KS ? issued_k - KS : 0; x < issued_k; ++x)
+            wait_drain(&ctl->k_full[x % KS], (x / KS) & 1, drain_ns);
+        for (int x = issued_v > VS ? issued_v - VS : 0; x < issued_v; ++x)
+            wait_drain(&ctl->v_full[x % VS], (x / VS) & 1, drain_ns);
+    }
     if (warp == kWarpPv && lane == 0) umma_commit(&ctl->drain);
     if (warp == kWarpMma) {
         if (lane == 0) {
