@@ -444,9 +444,9 @@ int atflash_cache_append_theta(const void *k, const int64_t *k_strides, const vo
  * sees, makes its dim non-finite in every node of that KV head (NaN, or the
  * infinity).  Pages beyond seqlens[b] + counts[b] are not looked up.
  * Accuracy: scores to about 2^-16 of the sum of their terms' sizes; probabilities to
- * 2^-16 where out_dtype is ATFLASH_F32 and for sequences of at most 128 committed
- * tokens (which hold every row that sees at most 128 keys), otherwise rounded to
- * bf16 once, which moves an output by at most 2^-8 of sum p |v|; sums in fp32.
+ * 2^-16 where out_dtype is ATFLASH_F32 and in every row that sees at most 128 keys
+ * (and others of its tile), otherwise rounded to bf16 once, which moves an output
+ * by at most 2^-8 of sum p |v|; sums in fp32.
  * Any Hq / Hkv; B*T*Hq <= 2^31 - 1.
  */
 size_t atflash_tree_decode_workspace_bytes(int B, int T, int Hq, int Hkv, int D);

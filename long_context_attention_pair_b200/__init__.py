@@ -637,7 +637,7 @@ def tree_decode_paged(q, kpages, vpages, block_table, seqlens, page_size: int, r
     (out, lse [B, Hq, T] fp32).  A node that sees nothing gets 0 and -inf.  ``workspace``:
     ``tree_decode_workspace_bytes`` bytes, not shared by calls that overlap; allocated
     here when absent or smaller.  An fp32 output keeps the probabilities to 2^-16; a bf16
-    one rounds them to bf16, save in sequences of at most 128 committed tokens.
+    one rounds them to bf16, save in rows that see at most 128 keys.
     """
     torch = _torch()
     B, T, Hq, D = q.shape

@@ -39,7 +39,7 @@
 //
 // Precision.  q~ is kept as two bf16 parts (hi + lo, 2^-16 of its value), so
 // scores carry fp32-grade error; sums, maxima and O are fp32.  So is P (two parts, two
-// MMAs for each 16 keys) for fp32 outputs and for sequences with rows that may see 128
+// MMAs for each 16 keys) for fp32 outputs and for row tiles with rows that may see 128
 // keys or fewer, where a rounding of P does not average out.  Otherwise P is rounded to
 // bf16 once, which moves an output by at most 2^-8 of sum p |v|, as much as its own
 // rounding to bf16 may.  On 8 ragged sequences of up to 8192 keys the rms error of bf16
